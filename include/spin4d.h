@@ -57,7 +57,9 @@ typedef enum spin4d_status {
     SPIN4D_ERR_BOUNDS = -7        /* checked build: a device bounds check failed */
 } spin4d_status;
 
-typedef enum spin4d_dtype { SPIN4D_F32 = 0, SPIN4D_F16 = 1 } spin4d_dtype;
+/* SPIN4D_BF16 is a type of the tensor-list calls (spin4d_grad_norm and its
+ * neighbours) alone; the decoders take SPIN4D_F32 and SPIN4D_F16. */
+typedef enum spin4d_dtype { SPIN4D_F32 = 0, SPIN4D_F16 = 1, SPIN4D_BF16 = 2 } spin4d_dtype;
 
 #define SPIN4D_MAX_LEVELS 16
 #define SPIN4D_MAX_FEATURES 8
@@ -275,6 +277,109 @@ int spin4d_cov_assemble(const float* scale, const float* rot, int64_t N, float* 
 int spin4d_adam_step(float* params, void* params_work, float* grad, float* m, float* v,
                      int64_t n, int step, float lr, float b1, float b2, float eps,
                      int zero_grad, int32_t* nonfinite_flag, spin4d_stream_t stream);
+
+/*
+ * The update over a list of tensors: a decoder's tables and weights, the
+ * positions, a gate's parameters, each with its gradient.  spin4d_grad_norm
+ * measures the gradients and writes a control block on the device;
+ * spin4d_clip_grads and spin4d_adam_step_tensors take the clipping
+ * coefficient (and the step count) from it, so nothing waits for the host and
+ * the sequence can be captured into a CUDA graph and replayed.
+ *
+ * The lists are host arrays, read during the call.  A list has at most
+ * SPIN4D_MAX_LIST_TENSORS tensors; a tensor has n >= 0 contiguous values
+ * (n == 0: its pointers are not looked at), at most 2^40, aligned to its
+ * type's size; a list spans at most about 2^42 values.  Any alignment beyond
+ * that is handled; arrays of one tensor that start at different offsets from
+ * a 32-byte (fp16 and bf16: 16-byte) boundary take a slower path.
+ */
+#define SPIN4D_MAX_LIST_TENSORS 65536
+
+/* spin4d_grad_norm's norm_type */
+#define SPIN4D_NORM_MAX 0       /* max |g| */
+#define SPIN4D_NORM_L1 1        /* sum |g| */
+#define SPIN4D_NORM_L2 2        /* sqrt(sum g^2) */
+
+typedef struct spin4d_grad_tensor {
+    const void* grad;       /* n values of grad_dtype */
+    void* out;              /* spin4d_clip_grads: n values of out_dtype; NULL: in place */
+    int64_t n;
+    int32_t grad_dtype;     /* SPIN4D_F32, SPIN4D_F16 or SPIN4D_BF16 */
+    int32_t out_dtype;
+} spin4d_grad_tensor;
+
+/* Device memory of the caller, 16-byte aligned; zeroed before its first use
+ * (step: set to the steps already taken when training resumes). */
+typedef struct spin4d_grad_control {
+    float norm;             /* of grad_scale * gradient over the whole list */
+    float coef;             /* clipped gradient = coef * stored gradient */
+    int32_t step;           /* steps taken: +1 by each spin4d_grad_norm whose norm is finite */
+    int32_t skipped;        /* +1 by each whose norm is not */
+} spin4d_grad_control;
+
+/* Bytes of spin4d_grad_norm's workspace (0 for an invalid count). */
+size_t spin4d_grad_norm_workspace(int count);
+
+/*
+ * norm = the norm of grad_scale * g over all tensors of the list, and
+ *   coef = grad_scale * min(1, max_norm / (norm + 1e-6)).
+ * grad_scale (> 0, finite) undoes a loss scale or averages a sum over ranks;
+ * max_norm >= 0, INFINITY to measure only.  Where the norm is not a finite
+ * fp32 number (a NaN or infinity in any gradient), coef is 0, `step` stays and
+ * `skipped` counts it.  norms (optional, `count` fp32 values): each tensor's
+ * own norm, likewise scaled.  Squares and sums are 64-bit and are added in an
+ * order that depends on the list and the device alone: the same gradients give
+ * the same bits.  A tensor listed twice counts twice.
+ *   workspace  device, spin4d_grad_norm_workspace(count) bytes, 256-byte
+ *              aligned, contents ignored on entry; calls that can overlap on
+ *              the GPU (other streams, captured graphs) need one each
+ * count == 0 measures nothing: norm 0, coef grad_scale (0 for max_norm == 0).
+ */
+int spin4d_grad_norm(const spin4d_grad_tensor* tensors, int count, int norm_type, double grad_scale,
+                     double max_norm, spin4d_grad_control* control, float* norms,
+                     void* workspace, size_t ws_bytes, spin4d_stream_t stream);
+
+/*
+ * out = control->coef * grad for every tensor, in fp32 and rounded to the
+ * output's type; coef == 0 writes zeros whatever the gradient holds, so that a
+ * gradient with a NaN is dropped whole.  SPIN4D_ERR_INVALID when an output
+ * overlaps another array of the list (its own gradient in the same type, that
+ * is in place, excepted).
+ */
+int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, const spin4d_grad_control* control,
+                      spin4d_stream_t stream);
+
+/* One tensor of spin4d_adam_step_tensors.  params, m, v: n fp32 values;
+ * params_work (optional): n values of work_dtype (SPIN4D_F16 or SPIN4D_BF16),
+ * the rounded copy of the updated parameters. */
+typedef struct spin4d_adam_tensor {
+    float* params;
+    void* params_work;
+    void* grad;
+    float* m;
+    float* v;
+    int64_t n;
+    float lr;
+    float weight_decay;
+    int32_t grad_dtype;
+    int32_t work_dtype;
+} spin4d_adam_tensor;
+
+/*
+ * spin4d_adam_step over a list, with decoupled weight decay (Loshchilov &
+ * Hutter) and, when `control` is given, on g = control->coef * grad:
+ *   m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2;
+ *   p -= lr * (m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps) + lr * weight_decay * p
+ * t = step when step > 0, else control->step (which spin4d_grad_norm has
+ * advanced).  Where control->norm is not finite (or t < 1) params, params_work,
+ * m and v stay as they are.  zero_grad != 0 clears the gradients in either
+ * case.  nonfinite_flag as in spin4d_adam_step.  SPIN4D_ERR_INVALID when an
+ * array that is written overlaps another one of the list; gradients that are
+ * not cleared may be shared.
+ */
+int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int count, int step, double b1, double b2,
+                             double eps, int zero_grad, const spin4d_grad_control* control,
+                             int32_t* nonfinite_flag, spin4d_stream_t stream);
 
 /*
  * HexPlane encoder + deformation network (4D Gaussian Splatting reading

@@ -8,7 +8,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional
+import struct
+from typing import Dict, Optional, Sequence, Union
 
 import torch
 
@@ -22,7 +23,7 @@ lib = ctypes.CDLL(_LIB_PATH)
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_NONFINITE, ERR_INJECTED, ERR_TIMEOUT, ERR_BOUNDS = (
     0, -1, -2, -3, -4, -5, -6, -7)
-F32, F16 = 0, 1
+F32, F16, BF16 = 0, 1, 2
 INPUT_NORMALISED = 1
 MAX_LEVELS = 16
 HEAD_ROWS = 11
@@ -97,6 +98,15 @@ class AdamGroup(ctypes.Structure):
     _fields_ = [("end", c_i64), ("lr", c_f32)]
 
 
+class GradTensor(ctypes.Structure):
+    _fields_ = [("grad", c_vp), ("out", c_vp), ("n", c_i64), ("grad_dtype", c_i32), ("out_dtype", c_i32)]
+
+
+class AdamTensor(ctypes.Structure):
+    _fields_ = [("params", c_vp), ("params_work", c_vp), ("grad", c_vp), ("m", c_vp), ("v", c_vp), ("n", c_i64),
+                ("lr", c_f32), ("weight_decay", c_f32), ("grad_dtype", c_i32), ("work_dtype", c_i32)]
+
+
 class Camera(ctypes.Structure):
     _fields_ = [("view", c_f32 * 12), ("fx", c_f32), ("fy", c_f32), ("cx", c_f32), ("cy", c_f32),
                 ("width", c_i32), ("height", c_i32), ("z_near", c_f32)]
@@ -134,6 +144,11 @@ _SIGS = {
     "spin4d_lr_warmup_cosine": (ctypes.c_double, [c_i64, ctypes.c_double, ctypes.c_double, c_i64, c_i64]),
     "spin4d_adam_step": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_f32, c_f32, c_f32, c_f32, c_i32,
                                  c_vp, c_vp]),
+    "spin4d_grad_norm_workspace": (c_sz, [c_i32]),
+    "spin4d_grad_norm": (c_i32, [c_vp, c_i32, c_i32, ctypes.c_double, ctypes.c_double, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "spin4d_clip_grads": (c_i32, [c_vp, c_i32, c_vp, c_vp]),
+    "spin4d_adam_step_tensors": (c_i32, [c_vp, c_i32, c_i32, ctypes.c_double, ctypes.c_double, ctypes.c_double, c_i32,
+                                         c_vp, c_vp, c_vp]),
     "spin4d_hexplane_plane_count": (c_i64, [P(HexDesc)]),
     "spin4d_hexplane_param_count": (c_i64, [P(HexDesc)]),
     "spin4d_hexplane_fwd": (c_i32, [P(HexDesc), c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, HexOutputs, c_vp]),
@@ -354,6 +369,192 @@ def adam_step_groups(params, grad, m, v, step: int, groups, b1: float, b2: float
 
 def lr_warmup_cosine(step: int, lr_max: float, lr_min: float, warmup: int, total: int) -> float:
     return float(lib.spin4d_lr_warmup_cosine(step, lr_max, lr_min, warmup, total))
+
+
+# ---- gradients to updated parameters, over a list of tensors ----
+_LIST_DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_NORMS = {"inf": 0, "l1": 1, "l2": 2}
+
+
+class _TensorList:
+    """A C array of tensor descriptors, the tensors it points at (kept alive)
+    and their device.  Built once for tensors that stay where they are."""
+
+    def _seal(self, struct_type, layout: str, values, tensors, count: int) -> None:
+        self.tensors = tensors
+        self.device = _one_device(tensors)
+        self._array = (struct_type * max(count, 1)).from_buffer_copy(
+            struct.pack("<" + layout * count, *values) if count else bytes(ctypes.sizeof(struct_type)))
+        self._count = count
+        self.address = ctypes.addressof(self._array)
+
+    def __len__(self) -> int:
+        return self._count
+
+
+def _one_device(tensors) -> Optional[torch.device]:
+    dev = None
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("the tensors of a list must be on one device")
+    return dev
+
+
+def _list_dtype(t: torch.Tensor, allowed=(torch.float32, torch.float16, torch.bfloat16)) -> int:
+    if t.dtype not in allowed:
+        raise ValueError("unsupported dtype %s" % t.dtype)
+    return _LIST_DT[t.dtype]
+
+
+class GradList(_TensorList):
+    """Gradients (float32, float16 or bfloat16) for grad_norm and clip_grads,
+    with the outputs that clip_grads writes (None: in place)."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        grads = list(grads)
+        outs = [None] * len(grads) if outs is None else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError("one output for each gradient")
+        values = []
+        for g, o in zip(grads, outs):
+            if o is not None and o.numel() != g.numel():
+                raise ValueError("an output has its gradient's size")
+            values += (_ptr(g) or 0, 0 if o is None else _ptr(o) or 0, g.numel(), _list_dtype(g),
+                       0 if o is None else _list_dtype(o))
+        self._seal(GradTensor, "QQqii", values, grads + [o for o in outs if o is not None], len(grads))
+
+
+class AdamList(_TensorList):
+    """Parameters and their state for adam_step_tensors."""
+
+    def __init__(self, params, grads, m, v, lr: Union[float, Sequence[float]],
+                 weight_decay: Union[float, Sequence[float]] = 0.0, params_work=None):
+        params, grads, m, v = list(params), list(grads), list(m), list(v)
+        n = len(params)
+        work = [None] * n if params_work is None else list(params_work)
+        rates = [list(x) if isinstance(x, (list, tuple)) else [float(x)] * n for x in (lr, weight_decay)]
+        if any(len(x) != n for x in [grads, m, v, work] + rates):
+            raise ValueError("one gradient, m, v, rate and working copy for each parameter tensor")
+        values = []
+        for p, g, mm, vv, w, r, d in zip(params, grads, m, v, work, *rates):
+            if any(x is not None and x.numel() != p.numel() for x in (g, mm, vv, w)):
+                raise ValueError("a parameter's gradient, state and working copy have its size")
+            for x in (p, mm, vv):
+                _list_dtype(x, (torch.float32,))
+            values += (_ptr(p) or 0, 0 if w is None else _ptr(w) or 0, _ptr(g) or 0, _ptr(mm) or 0, _ptr(vv) or 0,
+                       p.numel(), r, d, _list_dtype(g),
+                       0 if w is None else _list_dtype(w, (torch.float16, torch.bfloat16)))
+        self._seal(AdamTensor, "QQQQQqffii", values, params + grads + m + v + [w for w in work if w is not None], n)
+
+
+def grad_list(grads, outs=None) -> GradList:
+    """The gradients as grad_norm and clip_grads take them.  A program whose
+    gradients stay at their addresses builds it once and keeps it."""
+    return grads if isinstance(grads, GradList) and outs is None else GradList(grads, outs)
+
+
+def adam_list(params, grads, m, v, lr, weight_decay=0.0, params_work=None) -> AdamList:
+    """Parameters (float32), gradients (float32, float16, bfloat16), Adam's m
+    and v (float32) and the optional float16 or bfloat16 working copies.  lr
+    and weight_decay: one number, or one for each tensor."""
+    return AdamList(params, grads, m, v, lr, weight_decay, params_work)
+
+
+class GradControl:
+    """The control block of grad_norm, clip_grads and adam_step_tensors in
+    device memory.  norm, coef, step and skipped are 0-dim views of it: reading
+    them as numbers waits for the GPU, handing them to further work does not."""
+
+    def __init__(self, device="cuda", step: int = 0):
+        self.buf = torch.zeros(4, dtype=torch.int32, device=device)
+        if not self.buf.is_cuda:
+            raise ValueError("the control block must be on a CUDA device")
+        f = self.buf.view(torch.float32)
+        self.norm, self.coef, self.step, self.skipped = f[0], f[1], self.buf[2], self.buf[3]
+        if step:
+            self.step.fill_(step)
+        self.device = self.buf.device
+        self.address = self.buf.data_ptr()
+
+
+def grad_control(device="cuda", step: int = 0) -> GradControl:
+    """A control block; step: the steps already taken."""
+    return GradControl(device, step)
+
+
+def grad_norm_workspace(count: int) -> int:
+    return int(lib.spin4d_grad_norm_workspace(count))
+
+
+def _list_call(name: str, device: torch.device, stream, others, *args) -> None:
+    """The call on the list's device and stream.  ``others``: tensors that
+    have to be on that device too."""
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError("%s: every tensor must be on the list's device" % name)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        _check(name, getattr(lib, name)(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(name, getattr(lib, name)(*args, _stream(stream)))
+
+
+def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_type: str = "l2",
+              grad_scale: float = 1.0, norms: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> GradControl:
+    """The norm ("l2", "l1" or "inf") of grad_scale * gradient over all tensors
+    into ``control.norm`` and the clipping coefficient into ``control.coef``;
+    ``control.step`` goes up by one where the norm is finite,
+    ``control.skipped`` where it is not.  grads: a GradList or tensors.  norms:
+    a float32 tensor that gets each tensor's own norm.  The workspace (uint8
+    device tensor) is allocated when not given."""
+    grads = grad_list(grads)
+    if norm_type not in _NORMS:
+        raise ValueError("norm_type must be one of %s" % (sorted(_NORMS),))
+    if norms is not None and (norms.dtype != torch.float32 or norms.numel() != len(grads)):
+        raise ValueError("norms: one float32 value for each tensor")
+    device = control.device
+    if workspace is None:
+        workspace = torch.empty(grad_norm_workspace(len(grads)), dtype=torch.uint8, device=device)
+        if stream is not None:      # the allocator must not hand it on before that stream is done with it
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(_stream(stream), device))
+    if grads.device not in (None, device):
+        raise ValueError("spin4d_grad_norm: every tensor must be on the list's device")
+    _list_call("spin4d_grad_norm", device, stream, (norms, workspace), grads.address, len(grads),
+               _NORMS[norm_type], grad_scale, max_norm, control.address, _ptr(norms), _ptr(workspace),
+               workspace.numel() * workspace.element_size())
+    return control
+
+
+def clip_grads(grads, control: GradControl, stream=None) -> None:
+    """Multiplies every gradient by ``control.coef``, in place or into the
+    list's outputs; a coefficient of 0 writes zeros."""
+    grads = grad_list(grads)
+    if grads.device not in (None, control.device):
+        raise ValueError("spin4d_clip_grads: every tensor must be on the list's device")
+    _list_call("spin4d_clip_grads", control.device, stream, (), grads.address, len(grads), control.address)
+
+
+def adam_step_tensors(tensors: AdamList, b1: float, b2: float, eps: float, step: int = 0,
+                      control: Optional[GradControl] = None, zero_grad: bool = False,
+                      nonfinite_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One Adam step with decoupled weight decay over every tensor of the list.
+    With ``control`` the gradients are clipped by its coefficient, the step
+    count is its own when ``step`` is 0, and nothing but the clearing of
+    gradients happens where the norm was not finite."""
+    device = tensors.device
+    if device is None:
+        return
+    _list_call("spin4d_adam_step_tensors", device, stream, (None if control is None else control.buf, nonfinite_flag),
+               tensors.address, len(tensors), step, b1, b2, eps, 1 if zero_grad else 0,
+               None if control is None else control.address, _ptr(nonfinite_flag))
 
 
 # ---- the paper's four-head decoder ----
