@@ -315,6 +315,8 @@ typedef struct spin4d_grad_control {
     float coef;             /* clipped gradient = coef * stored gradient */
     int32_t step;           /* steps taken: +1 by each spin4d_grad_norm whose norm is finite */
     int32_t skipped;        /* +1 by each whose norm is not */
+    uint32_t ticket;        /* the library's: 0 between calls */
+    uint32_t reserved[3];
 } spin4d_grad_control;
 
 /* Bytes of spin4d_grad_norm's workspace (0 for an invalid count). */

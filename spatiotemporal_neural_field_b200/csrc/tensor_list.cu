@@ -4,11 +4,14 @@
 // copies nothing to the device first and a captured graph holds its own list.
 //
 // All three walk the same tiles: tensor k owns tile0[k+1] - tile0[k] tiles of
-// kTile values, and block b of G takes the tiles [T b / G, T (b+1) / G) of the
+// kTile values, and block b takes the tiles [per b, per (b+1)) of the
 // concatenation, whatever tensors they belong to.  A thread takes 8 values of a
 // tile.  Where every array of a tensor allows it, index 0 is moved down to a
 // 32-byte (16-bit types: 16-byte) boundary (`shift` values, skipped by the
 // first thread), so that views at odd offsets still move as vectors.
+//
+// The norm reads upwards, clip and Adam downwards: what the norm read last is
+// what the L2 still holds.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -16,6 +19,7 @@
 #include <new>
 
 #include "host.h"
+#include "pdl.cuh"
 
 namespace spin4d {
 namespace {
@@ -23,209 +27,248 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                       // values a thread takes of a tile
 constexpr int kTile = kThreads * kVec;
-constexpr int kMaxBlocks = 1184;              // slots of the norm's partial sums do not depend on the device
+constexpr int kMaxNormBlocks = 640;           // the norm's workspace does not depend on the device
 constexpr int kNormCap = 1024;                // tensors of one launch; longer lists take several
 constexpr int64_t kMaxValues = int64_t(1) << 40;
 constexpr int kMaxTensors = 1 << 16;
+#ifndef ADAM_PER
+#define ADAM_PER 64
+#endif
+#ifndef AH
+#define AH kKeep
+#endif
+#ifndef SH
+#define SH kKeep
+#endif
+#ifndef GH
+#define GH kKeep
+#endif
+#ifndef PAD
+#define PAD 3
+#endif
+#ifndef CLIP_PER
+#define CLIP_PER 32
+#endif
 
 __host__ __device__ inline int dtype_bytes(int dt) { return dt == SPIN4D_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------------------
 // Lists as the kernels see them
 // ---------------------------------------------------------------------------
-template <int CAP>
-struct NormList {
-  int count;
-  const void* ptr[CAP];
-  int64_t n[CAP];
-  uint32_t tile0[CAP + 1];
-  uint8_t dtype[CAP];
+// A tensor's length, types and the values that lie below index 0 in its first tile, in one word.
+constexpr int kStrided = 15;                  // instead of a shift: arrays that are not aligned alike
+struct Meta {
+  uint64_t bits;
+  __host__ __device__ int64_t n() const { return (int64_t)(bits & ((uint64_t(1) << 48) - 1)); }
+  __host__ __device__ int dtype() const { return (int)(bits >> 48) & 15; }
+  __host__ __device__ int out_dtype() const { return (int)(bits >> 52) & 15; }
+  __host__ __device__ int shift() const { return (int)(bits >> 56) & 15; }
+};
+Meta meta_of(int64_t n, int dtype, int out_dtype, int shift) {
+  return {(uint64_t)n | (uint64_t)dtype << 48 | (uint64_t)out_dtype << 52 | (uint64_t)shift << 56};
+}
+
+// What a kernel reads of one tensor lies together: each line of the constant bank that a block touches
+// for the first time costs it a round trip.
+struct NormEntry {
+  const void* a;
+  Meta meta;
+};
+struct ClipEntry {
+  const void* a;
+  void* out;
+  Meta meta;
+};
+struct alignas(64) AdamEntry {
+  float* p;
+  float* m;
+  float* v;
+  void* g;
+  void* work;
+  Meta meta;
+  float lr, decay;
 };
 
-template <int CAP>
-struct ClipList {
+constexpr int kHints = 128;
+template <typename Entry, int CAP>
+struct List {
   int count;
-  const void* src[CAP];
-  void* dst[CAP];
-  int64_t n[CAP];
+  uint32_t tiles;
+  uint32_t per;                               // tiles of a block
+  uint32_t hint_shift;                        // hint[t >> hint_shift]: a tensor at or before the tile's owner
   uint32_t tile0[CAP + 1];
-  uint8_t src_dtype[CAP], dst_dtype[CAP];
-  uint8_t shift[CAP];                         // values below index 0 of the aligned tile, or kStrided
-};
+  uint16_t hint[CAP > 16 ? kHints : 2];
+  Entry at[CAP];
 
-template <int CAP>
-struct AdamList {
-  int count;
-  float* p[CAP];
-  void* work[CAP];
-  void* g[CAP];
-  float* m[CAP];
-  float* v[CAP];
-  int64_t n[CAP];
-  float lr[CAP], decay[CAP];
-  uint32_t tile0[CAP + 1];
-  uint8_t g_dtype[CAP], work_dtype[CAP];
-  uint8_t shift[CAP];
-};
-constexpr int kStrided = 255;                 // arrays that are not aligned alike: a warp's lanes take every 32nd value
-
-// Last k with tile0[k] <= tile: the tensor that owns the tile (tensors without values own none).
-__device__ __forceinline__ int owner(const uint32_t* tile0, int count, uint32_t tile) {
-  int lo = 0, hi = count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tile0[mid] <= tile) lo = mid;
-    else hi = mid;
+  // The last tensor that begins at or before the tile: its owner (tensors without values own none).
+  __device__ __forceinline__ int owner(uint32_t tile) const {
+    int k = CAP > 16 ? hint[tile >> hint_shift] : 0;
+    while (k + 1 < count && tile0[k + 1] <= tile) ++k;
+    return k;
   }
-  return lo;
-}
-
-__device__ __forceinline__ uint32_t block_begin(uint32_t tiles, int b, int blocks) {
-  return (uint32_t)((uint64_t)tiles * (uint32_t)b / (uint32_t)blocks);
-}
-// The block whose range holds the tile: the largest b with block_begin(b) <= tile.
-__device__ __forceinline__ int block_of(uint32_t tiles, uint32_t tile, int blocks) {
-  return (int)((((uint64_t)tile + 1) * (uint32_t)blocks - 1) / tiles);
-}
+};
 
 // ---------------------------------------------------------------------------
 // Eight values at once
 // ---------------------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+// kStream: the line's next use is far off, so it is the first to leave L2 (a hint that 32-byte accesses have).
+enum Hint { kKeep, kStream };
 
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-template <typename T>
-__device__ __forceinline__ void load_vec(const T* a, float x[kVec]);
-template <>
-__device__ __forceinline__ void load_vec<float>(const float* a, float x[kVec]) {
-  const float4 u = reinterpret_cast<const float4*>(a)[0], w = reinterpret_cast<const float4*>(a)[1];
-  x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-  x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+// 8 values of 4 or 2 bytes as they are in memory.
+template <int BYTES>
+struct Raw {
+  uint32_t w[kVec * BYTES / 4];
+};
+template <Hint H>
+__device__ __forceinline__ void load_raw(const void* a, Raw<4>& r) {
+  if (H == kStream)
+    asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                   "=r"(r.w[7])
+                 : "l"(a) : "memory");
+  else
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                   "=r"(r.w[7])
+                 : "l"(a) : "memory");
 }
-template <>
-__device__ __forceinline__ void load_vec<__half>(const __half* a, float x[kVec]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(a);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+template <Hint H>
+__device__ __forceinline__ void load_raw(const void* a, Raw<2>& r) {
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+               : "l"(a) : "memory");
+}
+template <Hint H>
+__device__ __forceinline__ void store_raw(void* a, const Raw<4>& r) {
+  if (H == kStream)
+    asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(a),
+                 "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+                 : "memory");
+  else
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(a), "r"(r.w[0]), "r"(r.w[1]),
+                 "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+                 : "memory");
+}
+template <Hint H>
+__device__ __forceinline__ void store_raw(void* a, const Raw<2>& r) {
+  asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(a), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3])
+               : "memory");
+}
+
+// `bf`: 16-bit values are bfloat16, else fp16.
+__device__ __forceinline__ void unpack(const Raw<4>& r, bool, float x[kVec]) {
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) x[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ void unpack(const Raw<2>& r, bool bf, float x[kVec]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+    x[2 * i] = bf ? __uint_as_float(r.w[i] << 16) : f.x;
+    x[2 * i + 1] = bf ? __uint_as_float(r.w[i] & 0xffff0000u) : f.y;
   }
 }
-template <>
-__device__ __forceinline__ void load_vec<__nv_bfloat16>(const __nv_bfloat16* a, float x[kVec]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(a);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void pack(const float x[kVec], bool, Raw<4>& r) {
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) r.w[i] = __float_as_uint(x[i]);
+}
+__device__ __forceinline__ void pack(const float x[kVec], bool bf, Raw<2>& r) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    r.w[i] = bf ? *reinterpret_cast<const uint32_t*>(&b) : *reinterpret_cast<const uint32_t*>(&h);
   }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_vec(T* a, const float x[kVec]);
-template <>
-__device__ __forceinline__ void store_vec<float>(float* a, const float x[kVec]) {
-  reinterpret_cast<float4*>(a)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(a)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-template <>
-__device__ __forceinline__ void store_vec<__half>(__half* a, const float x[kVec]) {
-  __half2 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-  *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(h);
-}
-template <>
-__device__ __forceinline__ void store_vec<__nv_bfloat16>(__nv_bfloat16* a, const float x[kVec]) {
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-  *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(h);
 }
 
 // This thread's 8 places of one tile of a tensor of n values: first + i * stride for i in [0, 8),
 // those in [0, n).  `whole`: all of them are, and they are neighbours on a vector's boundary.
 struct Places {
-  int64_t first;
+  int64_t first, n;
   int stride;
   bool whole;
+  __device__ __forceinline__ Places(uint32_t tile, int shift, int64_t n_) : n(n_) {
+    const int64_t base = (int64_t)tile * kTile;
+    if (shift == kStrided) {
+      first = base + (threadIdx.x >> 5) * (32 * kVec) + (threadIdx.x & 31);
+      stride = 32;
+      whole = false;
+    } else {
+      first = base + threadIdx.x * kVec - shift;
+      stride = 1;
+      whole = first >= 0 && first + kVec <= n;
+    }
+  }
+  __device__ __forceinline__ int64_t place(int i) const { return first + (int64_t)i * stride; }
+  __device__ __forceinline__ bool has(int i) const { return place(i) >= 0 && place(i) < n; }
 };
-__device__ __forceinline__ Places places(uint32_t tile_in_tensor, int shift, int64_t n) {
-  Places q;
-  const int64_t base = (int64_t)tile_in_tensor * kTile;
-  if (shift == kStrided) {
-    q.first = base + (threadIdx.x >> 5) * (32 * kVec) + (threadIdx.x & 31);
-    q.stride = 32;
-    q.whole = false;
-  } else {
-    q.first = base + threadIdx.x * kVec - shift;
-    q.stride = 1;
-    q.whole = q.first >= 0 && q.first + kVec <= n;
-  }
-  return q;
-}
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* a, const Places& q, int64_t n, float x[kVec]) {
+// The values at the places; 0 for those outside [0, n).
+template <Hint H>
+__device__ __forceinline__ void fetch(const void* a, const Places& q, Raw<4>& r) {
   if (q.whole) {
-    load_vec<T>(a + q.first, x);
-    return;
-  }
+    load_raw<H>(static_cast<const float*>(a) + q.first, r);
+  } else {
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int64_t j = q.first + (int64_t)i * q.stride;
-    x[i] = j >= 0 && j < n ? to_f<T>(a[j]) : 0.0f;
+    for (int i = 0; i < kVec; ++i) r.w[i] = q.has(i) ? static_cast<const uint32_t*>(a)[q.place(i)] : 0u;
   }
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* a, const Places& q, int64_t n, const float x[kVec]) {
+template <Hint H>
+__device__ __forceinline__ void fetch(const void* a, const Places& q, Raw<2>& r) {
   if (q.whole) {
-    store_vec<T>(a + q.first, x);
-    return;
-  }
+    load_raw<H>(static_cast<const uint16_t*>(a) + q.first, r);
+  } else {
+    uint32_t h[kVec];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int64_t j = q.first + (int64_t)i * q.stride;
-    if (j >= 0 && j < n) a[j] = from_f<T>(x[i]);
+    for (int i = 0; i < kVec; ++i) h[i] = q.has(i) ? static_cast<const uint16_t*>(a)[q.place(i)] : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = h[2 * i] | h[2 * i + 1] << 16;
   }
 }
-__device__ __forceinline__ void load8(const void* a, int dt, const Places& q, int64_t n, float x[kVec]) {
-  if (dt == SPIN4D_F32) load8(static_cast<const float*>(a), q, n, x);
-  else if (dt == SPIN4D_F16) load8(static_cast<const __half*>(a), q, n, x);
-  else load8(static_cast<const __nv_bfloat16*>(a), q, n, x);
+template <Hint H>
+__device__ __forceinline__ void put(void* a, const Places& q, const Raw<4>& r) {
+  if (q.whole) {
+    store_raw<H>(static_cast<float*>(a) + q.first, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (q.has(i)) static_cast<uint32_t*>(a)[q.place(i)] = r.w[i];
+  }
 }
-__device__ __forceinline__ void store8(void* a, int dt, const Places& q, int64_t n, const float x[kVec]) {
-  if (dt == SPIN4D_F32) store8(static_cast<float*>(a), q, n, x);
-  else if (dt == SPIN4D_F16) store8(static_cast<__half*>(a), q, n, x);
-  else store8(static_cast<__nv_bfloat16*>(a), q, n, x);
+template <Hint H>
+__device__ __forceinline__ void put(void* a, const Places& q, const Raw<2>& r) {
+  if (q.whole) {
+    store_raw<H>(static_cast<uint16_t*>(a) + q.first, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (q.has(i)) static_cast<uint16_t*>(a)[q.place(i)] = (uint16_t)(r.w[i / 2] >> 16 * (i & 1));
+  }
+}
+template <Hint H>
+__device__ __forceinline__ void put(void* a, int dt, const Places& q, const float x[kVec]) {
+  if (dt == SPIN4D_F32) {
+    Raw<4> r;
+    pack(x, false, r);
+    put<H>(a, q, r);
+  } else {
+    Raw<2> r;
+    pack(x, dt == SPIN4D_BF16, r);
+    put<H>(a, q, r);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Norm.  Squares and sums are 64-bit: a square of any fp32 value and the sum
 // of 2^40 of them neither overflow nor vanish, and the sum's order does not
-// show in the 32-bit result.  No atomics: block b's part of tensor k goes to
-// slot b + k (along the walk over (b, k) one of the two grows at each part, so
-// no two parts share a slot), and one block adds the slots in a fixed order.
+// show in the 32-bit result.  No atomics on sums: block b's part of tensor k
+// goes to slot b + k (along the walk over (b, k) one of the two grows at each
+// part, so no two parts share a slot), and the block that finishes last adds
+// the slots in a fixed order, whichever block that is.
 // ---------------------------------------------------------------------------
 enum { kL1 = SPIN4D_NORM_L1, kL2 = SPIN4D_NORM_L2, kMax = SPIN4D_NORM_MAX };
+constexpr int kWarps = kThreads / 32;
+constexpr int kParts = 16;                    // tensors whose parts a block holds before it writes them out
 
 template <int NORM>
 __device__ __forceinline__ double join(double a, double b) {
@@ -233,118 +276,264 @@ __device__ __forceinline__ double join(double a, double b) {
   return a + b;
 }
 template <int NORM>
-__device__ __forceinline__ void take(double& acc, const float x[kVec]) {
+__device__ __forceinline__ void take(const float x[kVec], double acc[2]) {
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const double d = (double)x[i];
-    if (NORM == kL2) acc = fma(d, d, acc);
-    else acc = join<NORM>(acc, fabs(d));
+  for (int j = 0; j < kVec; ++j) {
+    const double d = (double)x[j];
+    acc[j & 1] = NORM == kL2 ? fma(d, d, acc[j & 1]) : join<NORM>(acc[j & 1], fabs(d));
   }
 }
-template <int NORM>
-__device__ __forceinline__ double warp_join(double a) {
+template <int NORM, int LANES>
+__device__ __forceinline__ double lanes_join(double a) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a = join<NORM>(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int o = LANES / 2; o > 0; o >>= 1) a = join<NORM>(a, __shfl_xor_sync(0xffffffffu, a, o));
   return a;
 }
 
-template <int CAP, int NORM>
-__global__ void __launch_bounds__(kThreads) norm_parts_kernel(const __grid_constant__ NormList<CAP> list,
-                                                              double* __restrict__ slots) {
-  __shared__ double part[kThreads / 32];
-  const uint32_t tiles = list.tile0[list.count];
-  uint32_t t = block_begin(tiles, blockIdx.x, gridDim.x);
-  const uint32_t end = block_begin(tiles, blockIdx.x + 1, gridDim.x);
-  if (t >= end) return;
-  for (int k = owner(list.tile0, list.count, t); t < end; ++k) {
-    const uint32_t stop = min(end, list.tile0[k + 1]);
-    if (t >= stop) continue;                  // a tensor without values
-    const int dt = list.dtype[k], bytes = dtype_bytes(dt);
-    const int64_t n = list.n[k];
-    const int shift = (int)((reinterpret_cast<uintptr_t>(list.ptr[k]) & (kVec * bytes - 1)) / bytes);
-    double acc = 0.0;
-    for (; t < stop; ++t) {
-      const Places q = places(t - list.tile0[k], shift, n);
+// This thread's part of tiles [t, stop) of one tensor.
+template <int NORM, int BYTES>
+__device__ __forceinline__ double norm_of_tiles(const void* a, const Meta meta, uint32_t t, uint32_t stop) {
+  constexpr int kAhead = 16 / BYTES;          // 32 registers of loads in flight
+  double acc[2] = {0.0, 0.0};
+  const int64_t n = meta.n();
+  const int shift = meta.shift();
+  const bool bf = meta.dtype() == SPIN4D_BF16;
+  const uint32_t head = t == 0 && shift != 0;                            // the first tile begins below index 0
+  const uint32_t whole = (uint32_t)min((uint64_t)stop, (uint64_t)(n + shift) / kTile);   // from here on it is partial
+  t += head;
+  const char* at = static_cast<const char*>(a) + ((int64_t)t * kTile + threadIdx.x * kVec - shift) * BYTES;
+  for (; t + kAhead <= whole; t += kAhead, at += kAhead * kTile * BYTES) {
+    Raw<BYTES> r[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load_raw<kKeep>(at + u * kTile * BYTES, r[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
       float x[kVec];
-      load8(list.ptr[k], dt, q, n, x);
-      take<NORM>(acc, x);
-    }
-    acc = warp_join<NORM>(acc);
-    __syncthreads();                          // the last tensor's parts have been read
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = acc;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kThreads / 32; ++w) acc = join<NORM>(acc, part[w]);
-      slots[blockIdx.x + k] = acc;
+      unpack(r[u], bf, x);
+      take<NORM>(x, acc);
     }
   }
+  // the first tile, those left over, the last
+  const uint32_t rest = head + (stop - t);
+  for (uint32_t i = 0; i < rest; i += 4) {
+    Raw<BYTES> r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i + u < rest) {
+        fetch<kKeep>(a, Places(i + u < head ? 0u : t + (i + u - head), shift, n), r[u]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec * BYTES / 4; ++j) r[u].w[j] = 0u;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x[kVec];
+      unpack(r[u], bf, x);
+      take<NORM>(x, acc);
+    }
+  }
+  return join<NORM>(acc[0], acc[1]);
 }
 
-struct FinishArgs {
+struct NormArgs {
   double grad_scale, max_norm;
-  int blocks, first, last;
+  int first, last;                            // launch of the list
   spin4d_grad_control* control;
   float* norms;                               // this launch's tensors' (may be null)
   double* total;                              // carried from launch to launch of one list
-  const double* slots;
+  double* slots;
 };
 
+// A kernel parameter read lane by lane: through its address, as memory, where the constant bank would
+// serve one lane at a time.
+template <typename T>
+__device__ __forceinline__ const T* as_memory(const T* p) {
+  asm volatile("" : "+l"(p));
+  return p;
+}
+
 template <int CAP, int NORM>
-__global__ void __launch_bounds__(1024) norm_finish_kernel(const __grid_constant__ NormList<CAP> list,
-                                                           const FinishArgs f) {
-  __shared__ double part[32];
-  const uint32_t tiles = list.tile0[list.count];
+__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ List<NormEntry, CAP> list,
+                                                           const NormArgs f) {
+  __shared__ double part[kParts][kWarps];
+  __shared__ int part_slot[kParts];
+  __shared__ bool is_last;
+  __shared__ double sums[kMaxNormBlocks + CAP];
+  __shared__ uint32_t tile0[CAP > 16 ? CAP + 1 : 1];
+  pdl_wait();
+  pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t per = list.per;
+  uint32_t t = blockIdx.x * per;
+  const uint32_t end = min(list.tiles, t + per);
+  double acc = 0.0;
+  int parts = 0;
+  // the warps walk through the block's tensors on their own; they meet when the parts are written out
+  auto write_parts = [&]() {
+    __syncthreads();
+    if (threadIdx.x < parts) {
+      double s = part[threadIdx.x][0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) s = join<NORM>(s, part[threadIdx.x][w]);
+      f.slots[part_slot[threadIdx.x]] = s;
+    }
+    __syncthreads();
+    parts = 0;
+  };
+  for (int k = list.owner(t); t < end; ++k) {
+    const uint32_t base = list.tile0[k], stop = min(end, list.tile0[k + 1]);
+    if (t >= stop) continue;                  // a tensor without values
+    const void* a = list.at[k].a;
+    const Meta meta = list.at[k].meta;
+    // its last tiles may be there only for balance
+    const uint32_t real = (uint32_t)((meta.n() + meta.shift() + kTile - 1) / kTile);
+    double one = 0.0;
+    if (t - base < real) {
+      if (meta.dtype() == SPIN4D_F32) one = norm_of_tiles<NORM, 4>(a, meta, t - base, min(stop - base, real));
+      else one = norm_of_tiles<NORM, 2>(a, meta, t - base, min(stop - base, real));
+    }
+    t = stop;
+    if (f.norms) {
+      one = lanes_join<NORM, 32>(one);
+      if (lane == 0) part[parts][warp] = one;
+      if (threadIdx.x == 0) part_slot[parts] = blockIdx.x + k;
+      if (++parts == kParts) write_parts();
+    } else {
+      acc = join<NORM>(acc, one);
+    }
+  }
+  if (!f.norms) {                             // only the whole is asked for: one slot for each block
+    acc = lanes_join<NORM, 32>(acc);
+    if (lane == 0) part[0][warp] = acc;
+    if (threadIdx.x == 0) part_slot[0] = blockIdx.x;
+    parts = 1;
+  }
+  write_parts();
+  // The last block to arrive finishes.  The ticket wraps to 0 for the next launch.
+  if (threadIdx.x == 0) {
+    uint32_t was;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                 : "=r"(was)
+                 : "l"(&f.control->ticket), "r"(gridDim.x - 1)
+                 : "memory");
+    is_last = was == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!is_last) return;
+  // All slots at once into shared memory: what follows is sums of few terms in a fixed order.
+  const int slots = list.tiles == 0 ? 0 : gridDim.x + (f.norms ? list.count - 1 : 0);
+  for (int i = threadIdx.x; i < slots; i += kThreads) sums[i] = __ldcg(&f.slots[i]);
+  if (CAP > 16 && f.norms) {
+    const uint32_t* starts = as_memory(list.tile0);
+    for (int k = threadIdx.x; k <= list.count; k += kThreads) tile0[k] = starts[k];
+  }
+  int32_t step = 0, skipped = 0;
+  if (threadIdx.x == 0) {
+    step = f.control->step;
+    skipped = f.control->skipped;
+  }
+  __syncthreads();
   double mine = 0.0;
-  for (int k = warp; k < list.count; k += 32) {
-    const uint32_t a = list.tile0[k], e = list.tile0[k + 1];
+  auto finish_tensor = [&](int k, double s) {
+    f.norms[k] = (float)(f.grad_scale * (NORM == kL2 ? sqrt(s) : s));
+    mine = join<NORM>(mine, s);
+  };
+  auto by_warp = [&](int k, uint32_t a, uint32_t e) {
     double s = 0.0;
     if (e > a) {
-      const int lb = block_of(tiles, e - 1, f.blocks);
-      for (int b = block_of(tiles, a, f.blocks) + lane; b <= lb; b += 32) s = join<NORM>(s, f.slots[b + k]);
+      const int b1 = (e - 1) / per;
+      for (int b = a / per + lane; b <= b1; b += 32) s = join<NORM>(s, sums[b + k]);
     }
-    s = warp_join<NORM>(s);
-    if (lane == 0 && f.norms) f.norms[k] = (float)(f.grad_scale * (NORM == kL2 ? sqrt(s) : s));
-    mine = join<NORM>(mine, s);
+    s = lanes_join<NORM, 32>(s);
+    if (lane == 0) finish_tensor(k, s);
+  };
+  if (!f.norms) {
+    for (int i = threadIdx.x; i < slots; i += kThreads) mine = join<NORM>(mine, sums[i]);
+  } else if (CAP <= 16) {
+    for (int k = warp; k < list.count; k += kWarps) by_warp(k, list.tile0[k], list.tile0[k + 1]);
+  } else {
+    // a thread for each tensor of few slots, a warp for each of the (few) others
+    for (int k = threadIdx.x; k < list.count; k += kThreads) {
+      const uint32_t a = tile0[k], e = tile0[k + 1];
+      if (e - a > 8 * per) continue;
+      double s = 0.0;
+      if (e > a) {
+        const int b1 = (e - 1) / per;
+        for (int b = a / per; b <= b1; ++b) s = join<NORM>(s, sums[b + k]);
+      }
+      finish_tensor(k, s);
+    }
+    for (int k0 = warp * 32; k0 < list.count; k0 += kThreads) {
+      const bool is_long = k0 + lane < list.count && tile0[k0 + lane + 1] - tile0[k0 + lane] > 8 * per;
+      for (uint32_t todo = __ballot_sync(0xffffffffu, is_long); todo; todo &= todo - 1) {
+        const int k = k0 + __ffs(todo) - 1;
+        by_warp(k, tile0[k], tile0[k + 1]);
+      }
+    }
   }
-  if (lane == 0) part[warp] = mine;
+  mine = lanes_join<NORM, 32>(mine);
+  if (lane == 0) part[0][warp] = mine;
   __syncthreads();
-  if (threadIdx.x != 0) return;
-  double total = f.first ? 0.0 : *f.total;
-  for (int w = 0; w < 32; ++w) total = join<NORM>(total, part[w]);
-  *f.total = total;
-  if (!f.last) return;
+  if (warp != 0) return;
+  double total = lanes_join<NORM, kWarps>(part[0][lane % kWarps]);
+  if (lane != 0) return;
+  if (!f.first) total = join<NORM>(*f.total, total);
+  if (!f.last) {
+    *f.total = total;
+    return;
+  }
   const double norm = f.grad_scale * (NORM == kL2 ? sqrt(total) : total);
   const float norm32 = (float)norm;
   const bool fine = isfinite(norm32);
   f.control->norm = norm32;
   f.control->coef = fine ? (float)(f.grad_scale * fmin(1.0, f.max_norm / (norm + 1e-6))) : 0.0f;
-  if (fine) f.control->step += 1;
-  else f.control->skipped += 1;
+  if (fine) f.control->step = step + 1;
+  else f.control->skipped = skipped + 1;
 }
 
 // ---------------------------------------------------------------------------
 // Clip: out = coef * gradient.
 // ---------------------------------------------------------------------------
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ ClipList<CAP> list,
-                                                        const spin4d_grad_control* __restrict__ control) {
-  const uint32_t tiles = list.tile0[list.count];
-  uint32_t t = block_begin(tiles, blockIdx.x, gridDim.x);
-  const uint32_t end = block_begin(tiles, blockIdx.x + 1, gridDim.x);
-  if (t >= end) return;
-  const float coef = control->coef;
-  for (int k = owner(list.tile0, list.count, t); t < end; ++k) {
-    const uint32_t stop = min(end, list.tile0[k + 1]);
-    for (; t < stop; ++t) {
-      const int64_t n = list.n[k];
-      const Places q = places(t - list.tile0[k], list.shift[k], n);
-      float x[kVec];
-      load8(list.src[k], list.src_dtype[k], q, n, x);
+// Tiles [t, stop) of one tensor, from the last down.
+template <int BYTES>
+__device__ __forceinline__ void clip_tiles(const void* a, void* o, const Meta meta, uint32_t t, uint32_t stop, float coef) {
+  constexpr int kAhead = 8 / BYTES;           // 16 registers of loads in flight
+  const int64_t n = meta.n();
+  const int shift = meta.shift();
+  while (stop > t) {
+    Raw<BYTES> r[kAhead];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = coef == 0.0f ? 0.0f : coef * x[i];   // zeros whatever the gradient holds
-      store8(list.dst[k], list.dst_dtype[k], q, n, x);
-    }
+    for (int u = 0; u < kAhead; ++u)
+      if (stop - t > u) fetch<kStream>(a, Places(stop - 1 - u, shift, n), r[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (stop - t > u) {
+        float x[kVec];
+        unpack(r[u], meta.dtype() == SPIN4D_BF16, x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[i] = coef == 0.0f ? 0.0f : coef * x[i];   // zeros whatever the gradient holds
+        put<kKeep>(o, meta.out_dtype(), Places(stop - 1 - u, shift, n), x);
+      }
+    stop -= min((uint32_t)kAhead, stop - t);
+  }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant__ List<ClipEntry, CAP> list,
+                                                           const spin4d_grad_control* control) {
+  pdl_wait();
+  pdl_release();
+  const uint32_t begin = (gridDim.x - 1 - blockIdx.x) * list.per;
+  uint32_t end = min(list.tiles, begin + list.per);
+  const float coef = control->coef;
+  for (int k = list.owner(end - 1); end > begin; --k) {
+    const uint32_t base = list.tile0[k], t = max(begin, base);
+    if (t >= end) continue;                   // a tensor without values
+    const ClipEntry& e = list.at[k];
+    if (e.meta.dtype() == SPIN4D_F32) clip_tiles<4>(e.a, e.out, e.meta, t - base, end - base, coef);
+    else clip_tiles<2>(e.a, e.out, e.meta, t - base, end - base, coef);
+    end = t;
   }
 }
 
@@ -361,37 +550,47 @@ struct AdamArgs {
 };
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) adam_list_kernel(const __grid_constant__ AdamList<CAP> list,
-                                                             const AdamArgs a) {
-  const uint32_t tiles = list.tile0[list.count];
-  uint32_t t = block_begin(tiles, blockIdx.x, gridDim.x);
-  const uint32_t end = block_begin(tiles, blockIdx.x + 1, gridDim.x);
-  if (t >= end) return;
-  float coef = 1.0f;
-  int step = a.step;
-  bool skip = false;
-  if (a.control) {
-    coef = a.control->coef;
-    if (step == 0) step = a.control->step;
-    skip = !isfinite(a.control->norm) || step < 1;
-  }
-  if (skip && !a.zero_grad) return;
-  // 1 - b^step = -expm1(step log b): the product in 64 bits, then within 2 ulp of fp32
-  const float inv_bc1 = 1.0f / -expm1f((float)(step * a.log_b1));
-  const float inv_bc2 = 1.0f / -expm1f((float)(step * a.log_b2));
-  bool bad = false;
-  for (int k = owner(list.tile0, list.count, t); t < end; ++k) {
-    const uint32_t stop = min(end, list.tile0[k + 1]);
-    for (; t < stop; ++t) {
-      const int64_t n = list.n[k];
-      const Places q = places(t - list.tile0[k], list.shift[k], n);
+__global__ void __launch_bounds__(kThreads, 3) adam_list_kernel(const __grid_constant__ List<AdamEntry, CAP> list,
+                                                                const AdamArgs a) {
+  pdl_wait();
+  pdl_release();
+  const uint32_t begin = (gridDim.x - 1 - blockIdx.x) * list.per;
+  uint32_t end = min(list.tiles, begin + list.per);
+  float coef = 1.0f, inv_bc1 = 0.0f, inv_bc2 = 0.0f;
+  bool ready = false, skip = false, bad = false;
+  for (int k = list.owner(end - 1); end > begin; --k) {
+    const uint32_t base = list.tile0[k], stop = max(begin, base);
+    if (stop >= end) continue;                // a tensor without values
+    const AdamEntry& e = list.at[k];
+    for (uint32_t t = end; t-- > stop;) {
+      const Places q(t - base, e.meta.shift(), e.meta.n());
+      Raw<4> rp, rm, rv, rg;
+      fetch<AH>(e.p, q, rp);
+      fetch<AH>(e.m, q, rm);
+      fetch<AH>(e.v, q, rv);
+      if (e.meta.dtype() == SPIN4D_F32) fetch<GH>(e.g, q, rg);
+      else fetch<GH>(e.g, q, reinterpret_cast<Raw<2>&>(rg));
+      if (!ready) {                           // behind the first loads, which do not wait for it
+        ready = true;
+        int step = a.step;
+        if (a.control) {
+          coef = a.control->coef;
+          if (step == 0) step = a.control->step;
+          skip = !isfinite(a.control->norm) || step < 1;
+        }
+        // 1 - b^step = -expm1(step log b): the product in 64 bits, then within 2 ulp of fp32
+        inv_bc1 = 1.0f / -expm1f((float)(step * a.log_b1));
+        inv_bc2 = 1.0f / -expm1f((float)(step * a.log_b2));
+      }
+      if (skip && !a.zero_grad) return;       // (the flag stays as it is)
       if (!skip) {
-        const float lr = list.lr[k], decay = lr * list.decay[k];
         float g[kVec], p[kVec], m[kVec], v[kVec];
-        load8(list.g[k], list.g_dtype[k], q, n, g);
-        load8(list.p[k], q, n, p);
-        load8(list.m[k], q, n, m);
-        load8(list.v[k], q, n, v);
+        unpack(rp, false, p);
+        unpack(rm, false, m);
+        unpack(rv, false, v);
+        if (e.meta.dtype() == SPIN4D_F32) unpack(rg, false, g);
+        else unpack(reinterpret_cast<Raw<2>&>(rg), e.meta.dtype() == SPIN4D_BF16, g);
+        const float lr = e.lr, decay = lr * e.decay;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           const float gi = coef == 0.0f ? 0.0f : coef * g[i];
@@ -399,21 +598,24 @@ __global__ void __launch_bounds__(kThreads) adam_list_kernel(const __grid_consta
           v[i] = a.b2 * v[i] + a.omb2 * (gi * gi);
           const float mh = m[i] * inv_bc1, vh = v[i] * inv_bc2;
           // outside [0, n) all four are 0: with eps = 0 the quotient is NaN there, which neither is stored nor flagged
-          const float r = p[i] - (lr * mh / (sqrtf(vh) + a.eps) + decay * p[i]);
-          const int64_t j = q.first + (int64_t)i * q.stride;
-          bad |= !isfinite(r) && (q.whole || (j >= 0 && j < n));
-          p[i] = r;
+          p[i] -= lr * mh / (sqrtf(vh) + a.eps) + decay * p[i];
+          bad |= !isfinite(p[i]) && (q.whole || q.has(i));
         }
-        store8(list.p[k], q, n, p);
-        store8(list.m[k], q, n, m);
-        store8(list.v[k], q, n, v);
-        if (list.work[k]) store8(list.work[k], list.work_dtype[k], q, n, p);
+        put<SH>(e.p, SPIN4D_F32, q, p);
+        put<SH>(e.m, SPIN4D_F32, q, m);
+        put<SH>(e.v, SPIN4D_F32, q, v);
+        if (e.work) {
+          Raw<2> w;
+          pack(p, e.meta.out_dtype() == SPIN4D_BF16, w);
+          put<kKeep>(e.work, q, w);
+        }
       }
       if (a.zero_grad) {
         const float zero[kVec] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        store8(list.g[k], list.g_dtype[k], q, n, zero);
+        put<kKeep>(e.g, e.meta.dtype(), q, zero);
       }
     }
+    end = stop;
   }
   if (a.flag && __syncthreads_or(bad) && threadIdx.x == 0) atomicExch(a.flag, 1);
 }
@@ -425,112 +627,185 @@ bool dtype_ok(int dt) { return dt == SPIN4D_F32 || dt == SPIN4D_F16 || dt == SPI
 
 bool array_ok(const void* p, int64_t n, int bytes) { return n == 0 || (p && aligned(p, bytes)); }
 
-// A stretch of memory that a call reads or writes.
-struct Stretch {
-  uintptr_t lo, hi;
-  bool write;
-};
-
-// Stretches, on the stack for short lists.  `ok` is false when the host has no memory for a long one.
-struct Stretches {
-  static constexpr int kLocal = 320;
-  Stretch local[kLocal];
-  Stretch* at;
-  int count = 0;
-  explicit Stretches(int most) : at(most <= kLocal ? local : new (std::nothrow) Stretch[most]) {}
+// The stretches of memory that a call reads or writes, family by family (all parameters, all gradients, ...).
+// A family is nearly always in the order of its addresses and apart from the others; only what is not gets
+// sorted or merged.  `ok` is false when the host has no memory for a long list.
+class Stretches {
+ public:
+  Stretches(int families, int count) : families_(families), count_(count) {
+    at_ = families * count <= kLocal ? local_ : new (std::nothrow) Stretch[(size_t)families * count];
+  }
   ~Stretches() {
-    if (at != local) delete[] at;
+    if (at_ != local_) delete[] at_;
   }
   Stretches(const Stretches&) = delete;
   Stretches& operator=(const Stretches&) = delete;
-  bool ok() const { return at != nullptr; }
-  void add(const void* p, int64_t n, int bytes, bool write) {
-    if (p && n > 0) at[count++] = {(uintptr_t)p, (uintptr_t)p + (uint64_t)n * bytes, write};
+  bool ok() const { return at_ != nullptr; }
+
+  void add(int family, bool write, const void* p, int64_t n, int bytes) {
+    if (!p || n == 0) return;
+    Family& f = family_[family];
+    const uintptr_t lo = (uintptr_t)p, hi = lo + (uint64_t)n * bytes;
+    f.write = write;
+    f.ordered = f.ordered && lo >= f.hi;
+    f.lo = f.count ? std::min(f.lo, lo) : lo;
+    f.hi = std::max(f.hi, hi);
+    at_[(size_t)family * count_ + f.count++] = {lo, hi};
   }
+
   // Whether something written is also another array's: blocks run in no order, so the result would have none.
   bool clash() {
-    std::sort(at, at + count, [](const Stretch& a, const Stretch& b) { return a.lo < b.lo; });
-    uintptr_t any = 0, written = 0;
-    for (int i = 0; i < count; ++i) {
-      if (at[i].lo < (at[i].write ? any : written)) return true;
-      any = std::max(any, at[i].hi);
-      if (at[i].write) written = std::max(written, at[i].hi);
+    int order[kFamilies], used = 0;
+    for (int i = 0; i < families_; ++i) {
+      Family& f = family_[i];
+      if (!f.count) continue;
+      order[used++] = i;
+      if (f.ordered) continue;
+      Stretch* at = at_ + (size_t)i * count_;
+      std::sort(at, at + f.count, [](const Stretch& a, const Stretch& b) { return a.lo < b.lo; });
+      if (f.write)
+        for (int k = 1; k < f.count; ++k)
+          if (at[k].lo < at[k - 1].hi) return true;
     }
-    return false;
+    std::sort(order, order + used, [this](int a, int b) { return family_[a].lo < family_[b].lo; });
+    bool apart = true;
+    for (int i = 1; i < used; ++i) apart = apart && family_[order[i]].lo >= family_[order[i - 1]].hi;
+    if (apart) return false;
+    // all of them in the order of their addresses
+    int next[kFamilies] = {};
+    uintptr_t any = 0, written = 0;
+    for (;;) {
+      int best = -1;
+      for (int i = 0; i < used; ++i) {
+        const int f = order[i];
+        if (next[f] < family_[f].count && (best < 0 || head(f, next).lo < head(best, next).lo)) best = f;
+      }
+      if (best < 0) return false;
+      const Stretch s = head(best, next);
+      ++next[best];
+      if (s.lo < (family_[best].write ? any : written)) return true;
+      any = std::max(any, s.hi);
+      if (family_[best].write) written = std::max(written, s.hi);
+    }
   }
+
+ private:
+  static constexpr int kLocal = 320, kFamilies = 5;
+  struct Stretch {
+    uintptr_t lo, hi;
+  };
+  struct Family {
+    int count = 0;
+    bool write = false, ordered = true;       // ordered: each begins where the last ended, or behind
+    uintptr_t lo = 0, hi = 0;
+  };
+  const Stretch& head(int family, const int* next) const { return at_[(size_t)family * count_ + next[family]]; }
+  int families_, count_;
+  Family family_[kFamilies];
+  Stretch local_[kLocal];
+  Stretch* at_;
 };
 
 int shift_of(const void* p, int bytes) { return (int)(((uintptr_t)p & (kVec * bytes - 1)) / bytes); }
 
-// Appends a tensor's tiles; false when the list holds more than a launch can number.
-bool add_tiles(uint32_t* tile0, int k, int64_t n, int shift) {
-  const int64_t tiles = n == 0 ? 0 : (n + shift + kTile - 1) / kTile;
-  const int64_t sum = (int64_t)tile0[k] + tiles;
-  tile0[k + 1] = (uint32_t)sum;
-  return sum < (int64_t(1) << 31);
+// Appends a tensor's tiles; the callers have checked that a list's sum fits.
+void add_tiles(uint32_t* tile0, int k, int64_t n, int shift) {
+  tile0[k + 1] = tile0[k] + (n == 0 ? 0u : (uint32_t)((n + (shift == kStrided ? 0 : shift) + kTile - 1) / kTile));
 }
 
-int blocks_for(uint32_t tiles) { return std::min(persistent_blocks(tiles, 8), kMaxBlocks); }
+// Splits the list over at most `most` blocks; returns how many.
+template <typename Entry, int CAP>
+int split(List<Entry, CAP>& list, int most) {
+  list.tiles = list.tile0[list.count];
+  list.per = std::max(1u, (list.tiles + most - 1) / most);
+  list.hint_shift = 0;
+  if (CAP > 16) {
+    while ((list.tiles >> list.hint_shift) >= (uint32_t)kHints) ++list.hint_shift;
+    int k = 0;
+    for (int h = 0; h < kHints; ++h) {
+      const uint64_t tile = (uint64_t)h << list.hint_shift;
+      while (k + 1 < list.count && list.tile0[k + 1] <= tile) ++k;
+      list.hint[h] = (uint16_t)k;
+    }
+  }
+  return (int)std::max(1u, (list.tiles + list.per - 1) / list.per);
+}
+
+// launch_pdl without copies of the list on the way.
+template <typename Kernel, typename... Args>
+int launch(Kernel kernel, int blocks, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* list[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+  return cuda_status(cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), list));
+}
 
 template <int CAP, int NORM>
-int norm_launches(const spin4d_grad_tensor* ts, int count, FinishArgs f, double* slots, cudaStream_t s) {
+int norm_launches(const spin4d_grad_tensor* ts, int count, NormArgs f, cudaStream_t s) {
   float* norms = f.norms;
   int at = 0;
   do {
-    NormList<CAP> list;
+    List<NormEntry, CAP> list;
     list.count = std::min(CAP, count - at);
     list.tile0[0] = 0;
     for (int k = 0; k < list.count; ++k) {
       const spin4d_grad_tensor& t = ts[at + k];
-      list.ptr[k] = t.grad;
-      list.n[k] = t.n;
-      list.dtype[k] = (uint8_t)t.grad_dtype;
-      if (!add_tiles(list.tile0, k, t.n, shift_of(t.grad, dtype_bytes(t.grad_dtype)))) return SPIN4D_ERR_INVALID;
+      const int shift = shift_of(t.grad, dtype_bytes(t.grad_dtype));
+      list.at[k] = {t.grad, meta_of(t.n, t.grad_dtype, 0, shift)};
+      add_tiles(list.tile0, k, t.n, shift);
     }
-    const uint32_t tiles = list.tile0[list.count];
-    f.blocks = blocks_for(tiles);
+    const int most = std::min(4 * sm_count(), kMaxNormBlocks);
+    // A block that begins another tensor waits for its first values once more, about PAD tiles' time: where
+    // blocks have several tiles, a tensor of a long list counts for that many more.
+    if (CAP > 16 && list.tile0[list.count] > (uint32_t)most) {
+      uint32_t more = 0;
+      for (int k = 0; k < list.count; ++k) {
+        const bool some = list.at[k].meta.n() > 0;
+        if (some) more += PAD;
+        list.tile0[k + 1] += more;
+      }
+    }
+    const int blocks = split(list, most);
     f.first = at == 0;
     f.last = at + list.count == count;
     f.norms = norms ? norms + at : nullptr;
-    if (tiles) {
-      norm_parts_kernel<CAP, NORM><<<f.blocks, kThreads, 0, s>>>(list, slots);
-      SPIN4D_CHECK(launch_status());
-    }
-    norm_finish_kernel<CAP, NORM><<<1, 1024, 0, s>>>(list, f);
-    SPIN4D_CHECK(launch_status());
+    SPIN4D_CHECK(launch(norm_kernel<CAP, NORM>, blocks, s, list, f));
     at += list.count;
   } while (at < count);
   return SPIN4D_OK;
 }
 
 template <int NORM>
-int norm_list(const spin4d_grad_tensor* ts, int count, const FinishArgs& f, double* slots, cudaStream_t s) {
-  if (count <= 16) return norm_launches<16, NORM>(ts, count, f, slots, s);
-  return norm_launches<kNormCap, NORM>(ts, count, f, slots, s);
+int norm_list(const spin4d_grad_tensor* ts, int count, const NormArgs& f, cudaStream_t s) {
+  if (count <= 16) return norm_launches<16, NORM>(ts, count, f, s);
+  return norm_launches<kNormCap, NORM>(ts, count, f, s);
 }
 
 template <int CAP>
 int clip_launches(const spin4d_grad_tensor* ts, int count, const spin4d_grad_control* control, cudaStream_t s) {
   for (int at = 0; at < count; at += CAP) {
-    ClipList<CAP> list;
+    List<ClipEntry, CAP> list;
     list.count = std::min(CAP, count - at);
     list.tile0[0] = 0;
     for (int k = 0; k < list.count; ++k) {
       const spin4d_grad_tensor& t = ts[at + k];
-      list.src[k] = t.grad;
-      list.dst[k] = t.out ? t.out : const_cast<void*>(t.grad);
-      list.n[k] = t.n;
-      list.src_dtype[k] = (uint8_t)t.grad_dtype;
-      list.dst_dtype[k] = (uint8_t)(t.out ? t.out_dtype : t.grad_dtype);
+      void* out = t.out ? t.out : const_cast<void*>(t.grad);
+      const int out_dtype = t.out ? t.out_dtype : t.grad_dtype;
       int shift = shift_of(t.grad, dtype_bytes(t.grad_dtype));
-      if (shift != shift_of(list.dst[k], dtype_bytes(list.dst_dtype[k]))) shift = kStrided;
-      list.shift[k] = (uint8_t)shift;
-      if (!add_tiles(list.tile0, k, t.n, shift == kStrided ? 0 : shift)) return SPIN4D_ERR_INVALID;
+      if (shift != shift_of(out, dtype_bytes(out_dtype))) shift = kStrided;
+      list.at[k] = {t.grad, out, meta_of(t.n, t.grad_dtype, out_dtype, shift)};
+      add_tiles(list.tile0, k, t.n, shift);
     }
-    const uint32_t tiles = list.tile0[list.count];
-    if (!tiles) continue;
-    clip_kernel<CAP><<<blocks_for(tiles), kThreads, 0, s>>>(list, control);
-    SPIN4D_CHECK(launch_status());
+    const int blocks = split(list, CLIP_PER * sm_count());
+    if (!list.tiles) continue;
+    SPIN4D_CHECK(launch(clip_kernel<CAP>, blocks, s, list, control));
   }
   return SPIN4D_OK;
 }
@@ -538,32 +813,22 @@ int clip_launches(const spin4d_grad_tensor* ts, int count, const spin4d_grad_con
 template <int CAP>
 int adam_launches(const spin4d_adam_tensor* ts, int count, const AdamArgs& a, cudaStream_t s) {
   for (int at = 0; at < count; at += CAP) {
-    AdamList<CAP> list;
+    List<AdamEntry, CAP> list;
     list.count = std::min(CAP, count - at);
     list.tile0[0] = 0;
     for (int k = 0; k < list.count; ++k) {
       const spin4d_adam_tensor& t = ts[at + k];
-      list.p[k] = t.params;
-      list.work[k] = t.params_work;
-      list.g[k] = t.grad;
-      list.m[k] = t.m;
-      list.v[k] = t.v;
-      list.n[k] = t.n;
-      list.lr[k] = t.lr;
-      list.decay[k] = t.weight_decay;
-      list.g_dtype[k] = (uint8_t)t.grad_dtype;
-      list.work_dtype[k] = (uint8_t)t.work_dtype;
       int shift = shift_of(t.params, 4);
       if (shift != shift_of(t.grad, dtype_bytes(t.grad_dtype)) || shift != shift_of(t.m, 4) ||
           shift != shift_of(t.v, 4) || (t.params_work && shift != shift_of(t.params_work, 2)))
         shift = kStrided;
-      list.shift[k] = (uint8_t)shift;
-      if (!add_tiles(list.tile0, k, t.n, shift == kStrided ? 0 : shift)) return SPIN4D_ERR_INVALID;
+      list.at[k] = {t.params, t.m, t.v, t.grad, t.params_work, meta_of(t.n, t.grad_dtype, t.work_dtype & 15, shift), t.lr,
+                    t.weight_decay};
+      add_tiles(list.tile0, k, t.n, shift);
     }
-    const uint32_t tiles = list.tile0[list.count];
-    if (!tiles) continue;
-    adam_list_kernel<CAP><<<blocks_for(tiles), kThreads, 0, s>>>(list, a);
-    SPIN4D_CHECK(launch_status());
+    const int blocks = split(list, ADAM_PER * sm_count());
+    if (!list.tiles) continue;
+    SPIN4D_CHECK(launch(adam_list_kernel<CAP>, blocks, s, list, a));
   }
   return SPIN4D_OK;
 }
@@ -575,7 +840,7 @@ using namespace spin4d;
 
 extern "C" size_t spin4d_grad_norm_workspace(int count) {
   if (count < 0 || count > kMaxTensors) return 0;
-  return sizeof(double) * (1 + kMaxBlocks + kNormCap);
+  return sizeof(double) * (1 + kMaxNormBlocks + kNormCap);
 }
 
 extern "C" int spin4d_grad_norm(const spin4d_grad_tensor* tensors, int count, int norm_type, double grad_scale,
@@ -595,25 +860,24 @@ extern "C" int spin4d_grad_norm(const spin4d_grad_tensor* tensors, int count, in
   }
   if (tiles >= (int64_t(1) << 31)) return SPIN4D_ERR_INVALID;
   if (fault_injected("spin4d_grad_norm")) return SPIN4D_ERR_INJECTED;
-  FinishArgs f = {};
+  NormArgs f = {};
   f.grad_scale = grad_scale;
   f.max_norm = max_norm;
   f.control = control;
   f.norms = norms;
   f.total = static_cast<double*>(workspace);
-  double* slots = static_cast<double*>(workspace) + 1;
-  f.slots = slots;
+  f.slots = static_cast<double*>(workspace) + 1;
   const cudaStream_t s = (cudaStream_t)stream;
-  if (norm_type == kL2) return norm_list<kL2>(tensors, count, f, slots, s);
-  if (norm_type == kL1) return norm_list<kL1>(tensors, count, f, slots, s);
-  return norm_list<kMax>(tensors, count, f, slots, s);
+  if (norm_type == kL2) return norm_list<kL2>(tensors, count, f, s);
+  if (norm_type == kL1) return norm_list<kL1>(tensors, count, f, s);
+  return norm_list<kMax>(tensors, count, f, s);
 }
 
 extern "C" int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, const spin4d_grad_control* control,
                                  spin4d_stream_t stream) {
   if (count < 0 || count > kMaxTensors || (count > 0 && !tensors)) return SPIN4D_ERR_INVALID;
   if (!control || !aligned(control, 16)) return SPIN4D_ERR_INVALID;
-  Stretches used(2 * count);
+  Stretches used(2, count);
   if (!used.ok()) return SPIN4D_ERR_INVALID;
   int64_t tiles = 0;
   for (int k = 0; k < count; ++k) {
@@ -623,10 +887,10 @@ extern "C" int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, c
     if (!array_ok(t.grad, t.n, dtype_bytes(t.grad_dtype))) return SPIN4D_ERR_INVALID;
     if (t.out && !array_ok(t.out, t.n, dtype_bytes(t.out_dtype))) return SPIN4D_ERR_INVALID;
     if (!t.out || (t.out == t.grad && t.out_dtype == t.grad_dtype)) {
-      used.add(t.grad, t.n, dtype_bytes(t.grad_dtype), true);
+      used.add(0, true, t.grad, t.n, dtype_bytes(t.grad_dtype));
     } else {
-      used.add(t.grad, t.n, dtype_bytes(t.grad_dtype), false);
-      used.add(t.out, t.n, dtype_bytes(t.out_dtype), true);
+      used.add(1, false, t.grad, t.n, dtype_bytes(t.grad_dtype));
+      used.add(0, true, t.out, t.n, dtype_bytes(t.out_dtype));
     }
     tiles += t.n / kTile + 2;
   }
@@ -645,7 +909,7 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
   if (!(b1 >= 0.0 && (float)b1 < 1.0f && b2 >= 0.0 && (float)b2 < 1.0f && eps >= 0.0 && isfinite((float)eps)))
     return SPIN4D_ERR_INVALID;
   if ((control && !aligned(control, 16)) || (nonfinite_flag && !aligned(nonfinite_flag, 4))) return SPIN4D_ERR_INVALID;
-  Stretches used(5 * count);
+  Stretches used(5, count);
   if (!used.ok()) return SPIN4D_ERR_INVALID;
   int64_t tiles = 0;
   for (int k = 0; k < count; ++k) {
@@ -657,11 +921,11 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
     if (!array_ok(t.params, t.n, 4) || !array_ok(t.m, t.n, 4) || !array_ok(t.v, t.n, 4) ||
         !array_ok(t.grad, t.n, dtype_bytes(t.grad_dtype)))
       return SPIN4D_ERR_INVALID;
-    used.add(t.params, t.n, 4, true);
-    used.add(t.m, t.n, 4, true);
-    used.add(t.v, t.n, 4, true);
-    used.add(t.params_work, t.n, 2, true);
-    used.add(t.grad, t.n, dtype_bytes(t.grad_dtype), zero_grad != 0);
+    used.add(0, true, t.params, t.n, 4);
+    used.add(1, true, t.m, t.n, 4);
+    used.add(2, true, t.v, t.n, 4);
+    used.add(3, true, t.params_work, t.n, 2);
+    used.add(4, zero_grad != 0, t.grad, t.n, dtype_bytes(t.grad_dtype));
     tiles += t.n / kTile + 2;
   }
   if (tiles >= (int64_t(1) << 31) || used.clash()) return SPIN4D_ERR_INVALID;
@@ -679,5 +943,5 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
   a.control = control;
   a.flag = nonfinite_flag;
   if (count <= 16) return adam_launches<16>(tensors, count, a, (cudaStream_t)stream);
-  return adam_launches<512>(tensors, count, a, (cudaStream_t)stream);
+  return adam_launches<448>(tensors, count, a, (cudaStream_t)stream);
 }

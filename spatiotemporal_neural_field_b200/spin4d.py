@@ -378,18 +378,20 @@ _NORMS = {"inf": 0, "l1": 1, "l2": 2}
 
 class _TensorList:
     """A C array of tensor descriptors, the tensors it points at (kept alive)
-    and their device.  Built once for tensors that stay where they are."""
+    and their device (None for an empty list).  Built once for tensors that
+    stay where they are."""
 
     def _seal(self, struct_type, layout: str, values, tensors, count: int) -> None:
         self.tensors = tensors
         self.device = _one_device(tensors)
+        self.index = None if self.device is None else self.device.index
         self._array = (struct_type * max(count, 1)).from_buffer_copy(
             struct.pack("<" + layout * count, *values) if count else bytes(ctypes.sizeof(struct_type)))
-        self._count = count
+        self.count = count
         self.address = ctypes.addressof(self._array)
 
     def __len__(self) -> int:
-        return self._count
+        return self.count
 
 
 def _one_device(tensors) -> Optional[torch.device]:
@@ -470,7 +472,7 @@ class GradControl:
     them as numbers waits for the GPU, handing them to further work does not."""
 
     def __init__(self, device="cuda", step: int = 0):
-        self.buf = torch.zeros(4, dtype=torch.int32, device=device)
+        self.buf = torch.zeros(8, dtype=torch.int32, device=device)
         if not self.buf.is_cuda:
             raise ValueError("the control block must be on a CUDA device")
         f = self.buf.view(torch.float32)
@@ -478,6 +480,7 @@ class GradControl:
         if step:
             self.step.fill_(step)
         self.device = self.buf.device
+        self.index = self.device.index
         self.address = self.buf.data_ptr()
 
 
@@ -490,19 +493,27 @@ def grad_norm_workspace(count: int) -> int:
     return int(lib.spin4d_grad_norm_workspace(count))
 
 
-def _list_call(name: str, device: torch.device, stream, others, *args) -> None:
-    """The call on the list's device and stream.  ``others``: tensors that
-    have to be on that device too."""
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError("%s: every tensor must be on the list's device" % name)
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        _check(name, getattr(lib, name)(*args, _stream(stream)))
+def _on_device(index: int, t: torch.Tensor, what: str) -> int:
+    if t.get_device() != index:
+        raise ValueError("%s must be on the list's device" % what)
+    return _ptr(t)
+
+
+# torch.cuda.current_stream and current_device build objects; these give the numbers
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _list_call(name: str, function, index: int, stream, *args) -> None:
+    """The call on the list's device, on the given stream or the device's current one."""
+    if _current_device() == index:
+        status = function(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
-            _check(name, getattr(lib, name)(*args, _stream(stream)))
+        with torch.cuda.device(index):
+            status = function(*args, _raw_stream(index) if stream is None else _stream(stream))
+    if status != OK:
+        raise Spin4dError(name, status)
 
 
 def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_type: str = "l2",
@@ -514,21 +525,25 @@ def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_
     ``control.skipped`` where it is not.  grads: a GradList or tensors.  norms:
     a float32 tensor that gets each tensor's own norm.  The workspace (uint8
     device tensor) is allocated when not given."""
-    grads = grad_list(grads)
-    if norm_type not in _NORMS:
+    if type(grads) is not GradList:
+        grads = GradList(grads)
+    kind = _NORMS.get(norm_type)
+    if kind is None:
         raise ValueError("norm_type must be one of %s" % (sorted(_NORMS),))
-    if norms is not None and (norms.dtype != torch.float32 or norms.numel() != len(grads)):
-        raise ValueError("norms: one float32 value for each tensor")
-    device = control.device
+    index = control.index
+    if grads.index is not None and grads.index != index:
+        raise ValueError("the control block must be on the list's device")
+    if norms is not None:
+        if norms.dtype != torch.float32 or norms.numel() != grads.count:
+            raise ValueError("norms: one float32 value for each tensor")
+        norms = _on_device(index, norms, "norms") or None
     if workspace is None:
-        workspace = torch.empty(grad_norm_workspace(len(grads)), dtype=torch.uint8, device=device)
+        workspace = torch.empty(grad_norm_workspace(grads.count), dtype=torch.uint8, device=control.device)
         if stream is not None:      # the allocator must not hand it on before that stream is done with it
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(_stream(stream), device))
-    if grads.device not in (None, device):
-        raise ValueError("spin4d_grad_norm: every tensor must be on the list's device")
-    _list_call("spin4d_grad_norm", device, stream, (norms, workspace), grads.address, len(grads),
-               _NORMS[norm_type], grad_scale, max_norm, control.address, _ptr(norms), _ptr(workspace),
+                                    else torch.cuda.ExternalStream(_stream(stream), control.device))
+    _list_call("spin4d_grad_norm", lib.spin4d_grad_norm, index, stream, grads.address, grads.count, kind, grad_scale,
+               max_norm, control.address, norms, _on_device(index, workspace, "the workspace"),
                workspace.numel() * workspace.element_size())
     return control
 
@@ -536,10 +551,12 @@ def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_
 def clip_grads(grads, control: GradControl, stream=None) -> None:
     """Multiplies every gradient by ``control.coef``, in place or into the
     list's outputs; a coefficient of 0 writes zeros."""
-    grads = grad_list(grads)
-    if grads.device not in (None, control.device):
-        raise ValueError("spin4d_clip_grads: every tensor must be on the list's device")
-    _list_call("spin4d_clip_grads", control.device, stream, (), grads.address, len(grads), control.address)
+    if type(grads) is not GradList:
+        grads = GradList(grads)
+    if grads.index is not None and grads.index != control.index:
+        raise ValueError("the control block must be on the list's device")
+    _list_call("spin4d_clip_grads", lib.spin4d_clip_grads, control.index, stream, grads.address, grads.count,
+               control.address)
 
 
 def adam_step_tensors(tensors: AdamList, b1: float, b2: float, eps: float, step: int = 0,
@@ -549,12 +566,15 @@ def adam_step_tensors(tensors: AdamList, b1: float, b2: float, eps: float, step:
     With ``control`` the gradients are clipped by its coefficient, the step
     count is its own when ``step`` is 0, and nothing but the clearing of
     gradients happens where the norm was not finite."""
-    device = tensors.device
-    if device is None:
+    index = tensors.index
+    if index is None:
         return
-    _list_call("spin4d_adam_step_tensors", device, stream, (None if control is None else control.buf, nonfinite_flag),
-               tensors.address, len(tensors), step, b1, b2, eps, 1 if zero_grad else 0,
-               None if control is None else control.address, _ptr(nonfinite_flag))
+    if control is not None and control.index != index:
+        raise ValueError("the control block must be on the list's device")
+    if nonfinite_flag is not None:
+        nonfinite_flag = _on_device(index, nonfinite_flag, "the flag")
+    _list_call("spin4d_adam_step_tensors", lib.spin4d_adam_step_tensors, index, stream, tensors.address, tensors.count,
+               step, b1, b2, eps, 1 if zero_grad else 0, None if control is None else control.address, nonfinite_flag)
 
 
 # ---- the paper's four-head decoder ----
