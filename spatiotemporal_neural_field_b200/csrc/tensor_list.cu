@@ -31,24 +31,15 @@ constexpr int kMaxNormBlocks = 640;           // the norm's workspace does not d
 constexpr int kNormCap = 1024;                // tensors of one launch; longer lists take several
 constexpr int64_t kMaxValues = int64_t(1) << 40;
 constexpr int kMaxTensors = 1 << 16;
-#ifndef ADAM_PER
-#define ADAM_PER 64
-#endif
-#ifndef AH
-#define AH kKeep
-#endif
-#ifndef SH
-#define SH kKeep
-#endif
-#ifndef GH
-#define GH kKeep
-#endif
-#ifndef PAD
-#define PAD 3
-#endif
-#ifndef CLIP_PER
-#define CLIP_PER 32
-#endif
+
+// Blocks of a launch, at most, for each SM.  The norm's are all resident at once (64 registers a thread), each
+// writes slots that one block adds in the end.  Clip and Adam meet nowhere: short blocks that the hardware hands
+// out as others end keep loads and stores mixed and both dies busy.  Adam over 134M parameters: 669 us with 3
+// a SM (all resident), 618 with 32, 602 with 64, 595 with 128; clip of 16.8M fp16 into fp32 with its norm:
+// 36.0 us with 4, 29.7 with 8, 30.2 with 12, 31.2 with 32, 35.6 with 64.
+constexpr int kNormBlocks = 4, kClipBlocks = 8, kAdamBlocks = 96;
+// Tiles that a tensor of a long list counts for besides its own (see norm_launches).
+constexpr uint32_t kTensorTiles = 4;
 
 __host__ __device__ inline int dtype_bytes(int dt) { return dt == SPIN4D_F32 ? 4 : 2; }
 
@@ -111,7 +102,9 @@ struct List {
 // ---------------------------------------------------------------------------
 // Eight values at once
 // ---------------------------------------------------------------------------
-// kStream: the line's next use is far off, so it is the first to leave L2 (a hint that 32-byte accesses have).
+// kStream: the line's next use is far off, so it is the first to leave L2.  32-byte accesses say so; a 16-byte
+// load that skips L1 does it too (an fp16 gradient read that way by the norm was gone when clip came: 34.0 us
+// for both over 16.8M values, 31.2 read plainly).
 enum Hint { kKeep, kStream };
 
 // 8 values of 4 or 2 bytes as they are in memory.
@@ -134,9 +127,14 @@ __device__ __forceinline__ void load_raw(const void* a, Raw<4>& r) {
 }
 template <Hint H>
 __device__ __forceinline__ void load_raw(const void* a, Raw<2>& r) {
-  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
-               : "l"(a) : "memory");
+  if (H == kStream)
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(a) : "memory");
+  else
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(a) : "memory");
 }
 template <Hint H>
 __device__ __forceinline__ void store_raw(void* a, const Raw<4>& r) {
@@ -202,6 +200,11 @@ struct Places {
   __device__ __forceinline__ int64_t place(int i) const { return first + (int64_t)i * stride; }
   __device__ __forceinline__ bool has(int i) const { return place(i) >= 0 && place(i) < n; }
 };
+
+// Into L2 ahead of the loads: a launch that overlaps the kernel before it may not read yet, but may ask.
+__device__ __forceinline__ void warm(const void* a, const Places& q, int bytes) {
+  if (q.whole) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a) + q.first * bytes));
+}
 
 // The values at the places; 0 for those outside [0, n).
 template <Hint H>
@@ -361,12 +364,18 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
   __shared__ bool is_last;
   __shared__ double sums[kMaxNormBlocks + CAP];
   __shared__ uint32_t tile0[CAP > 16 ? CAP + 1 : 1];
-  pdl_wait();
-  pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t per = list.per;
   uint32_t t = blockIdx.x * per;
   const uint32_t end = min(list.tiles, t + per);
+  const int owner = list.owner(t);
+  if (t < end) {
+    const NormEntry& e = list.at[owner];
+    for (uint32_t i = t; i < min(end, t + 4); ++i)
+      warm(e.a, Places(i - list.tile0[owner], e.meta.shift(), e.meta.n()), dtype_bytes(e.meta.dtype()));
+  }
+  pdl_wait();
+  pdl_release();
   double acc = 0.0;
   int parts = 0;
   // the warps walk through the block's tensors on their own; they meet when the parts are written out
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
     __syncthreads();
     parts = 0;
   };
-  for (int k = list.owner(t); t < end; ++k) {
+  for (int k = owner; t < end; ++k) {
     const uint32_t base = list.tile0[k], stop = min(end, list.tile0[k + 1]);
     if (t >= stop) continue;                  // a tensor without values
     const void* a = list.at[k].a;
@@ -422,16 +431,37 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
   __syncthreads();
   if (!is_last) return;
   // All slots at once into shared memory: what follows is sums of few terms in a fixed order.
+  constexpr int kSlotLoads = (kMaxNormBlocks + CAP + kThreads - 1) / kThreads;
+  constexpr int kTileLoads = CAP > 16 ? CAP / kThreads + 1 : 0;
   const int slots = list.tiles == 0 ? 0 : gridDim.x + (f.norms ? list.count - 1 : 0);
-  for (int i = threadIdx.x; i < slots; i += kThreads) sums[i] = __ldcg(&f.slots[i]);
-  if (CAP > 16 && f.norms) {
-    const uint32_t* starts = as_memory(list.tile0);
-    for (int k = threadIdx.x; k <= list.count; k += kThreads) tile0[k] = starts[k];
+  const int starts = f.norms ? list.count + 1 : 0;
+  double slot[kSlotLoads];
+  uint32_t start[kTileLoads + 1];
+#pragma unroll
+  for (int j = 0; j < kSlotLoads; ++j) {
+    const int i = threadIdx.x + j * kThreads;
+    slot[j] = i < slots ? __ldcg(&f.slots[i]) : 0.0;
+  }
+  const uint32_t* from = as_memory(list.tile0);
+#pragma unroll
+  for (int j = 0; j < kTileLoads; ++j) {
+    const int k = threadIdx.x + j * kThreads;
+    start[j] = k < starts ? from[k] : 0u;
   }
   int32_t step = 0, skipped = 0;
   if (threadIdx.x == 0) {
     step = f.control->step;
     skipped = f.control->skipped;
+  }
+#pragma unroll
+  for (int j = 0; j < kSlotLoads; ++j) {
+    const int i = threadIdx.x + j * kThreads;
+    if (i < slots) sums[i] = slot[j];
+  }
+#pragma unroll
+  for (int j = 0; j < kTileLoads; ++j) {
+    const int k = threadIdx.x + j * kThreads;
+    if (k < starts) tile0[k] = start[j];
   }
   __syncthreads();
   double mine = 0.0;
@@ -513,6 +543,7 @@ __device__ __forceinline__ void clip_tiles(const void* a, void* o, const Meta me
         unpack(r[u], meta.dtype() == SPIN4D_BF16, x);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) x[i] = coef == 0.0f ? 0.0f : coef * x[i];   // zeros whatever the gradient holds
+        // kept: the optimiser reads it next (norm, clip and Adam of 4M values 28.9 us, streamed 30.0)
         put<kKeep>(o, meta.out_dtype(), Places(stop - 1 - u, shift, n), x);
       }
     stop -= min((uint32_t)kAhead, stop - t);
@@ -540,6 +571,16 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Adam with decoupled weight decay.
 // ---------------------------------------------------------------------------
+// The square root within 2^-23 of itself (subnormal arguments too).  With it and a quotient within 2 ulp a step
+// is off by at most 5 roundings more than with the correctly rounded ones, 2^-22 of what it moves a parameter, of which a
+// parameter's own rounding usually leaves nothing; both rounded correctly take most of the kernel's instructions:
+// norm and update of 16.8M parameters 101.4 us, of the smallest decoder 8.0, so 89.6 and 6.4.
+__device__ __forceinline__ float root(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 struct AdamArgs {
   float b1, b2, omb1, omb2, eps;
   double log_b1, log_b2;                      // for a step that only the device knows
@@ -552,24 +593,32 @@ struct AdamArgs {
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 3) adam_list_kernel(const __grid_constant__ List<AdamEntry, CAP> list,
                                                                 const AdamArgs a) {
-  pdl_wait();
-  pdl_release();
   const uint32_t begin = (gridDim.x - 1 - blockIdx.x) * list.per;
   uint32_t end = min(list.tiles, begin + list.per);
+  const int last = list.owner(end - 1);
+  {
+    const AdamEntry& e = list.at[last];
+    const Places q(end - 1 - list.tile0[last], e.meta.shift(), e.meta.n());
+    warm(e.p, q, 4);
+    warm(e.m, q, 4);
+    warm(e.v, q, 4);
+  }
+  pdl_wait();
+  pdl_release();
   float coef = 1.0f, inv_bc1 = 0.0f, inv_bc2 = 0.0f;
   bool ready = false, skip = false, bad = false;
-  for (int k = list.owner(end - 1); end > begin; --k) {
+  for (int k = last; end > begin; --k) {
     const uint32_t base = list.tile0[k], stop = max(begin, base);
     if (stop >= end) continue;                // a tensor without values
     const AdamEntry& e = list.at[k];
     for (uint32_t t = end; t-- > stop;) {
       const Places q(t - base, e.meta.shift(), e.meta.n());
       Raw<4> rp, rm, rv, rg;
-      fetch<AH>(e.p, q, rp);
-      fetch<AH>(e.m, q, rm);
-      fetch<AH>(e.v, q, rv);
-      if (e.meta.dtype() == SPIN4D_F32) fetch<GH>(e.g, q, rg);
-      else fetch<GH>(e.g, q, reinterpret_cast<Raw<2>&>(rg));
+      fetch<kKeep>(e.p, q, rp);
+      fetch<kKeep>(e.m, q, rm);
+      fetch<kKeep>(e.v, q, rv);
+      if (e.meta.dtype() == SPIN4D_F32) fetch<kKeep>(e.g, q, rg);
+      else fetch<kKeep>(e.g, q, reinterpret_cast<Raw<2>&>(rg));
       if (!ready) {                           // behind the first loads, which do not wait for it
         ready = true;
         int step = a.step;
@@ -598,12 +647,12 @@ __global__ void __launch_bounds__(kThreads, 3) adam_list_kernel(const __grid_con
           v[i] = a.b2 * v[i] + a.omb2 * (gi * gi);
           const float mh = m[i] * inv_bc1, vh = v[i] * inv_bc2;
           // outside [0, n) all four are 0: with eps = 0 the quotient is NaN there, which neither is stored nor flagged
-          p[i] -= lr * mh / (sqrtf(vh) + a.eps) + decay * p[i];
+          p[i] -= __fdividef(lr * mh, root(vh) + a.eps) + decay * p[i];
           bad |= !isfinite(p[i]) && (q.whole || q.has(i));
         }
-        put<SH>(e.p, SPIN4D_F32, q, p);
-        put<SH>(e.m, SPIN4D_F32, q, m);
-        put<SH>(e.v, SPIN4D_F32, q, v);
+        put<kKeep>(e.p, SPIN4D_F32, q, p);
+        put<kKeep>(e.m, SPIN4D_F32, q, m);
+        put<kKeep>(e.v, SPIN4D_F32, q, v);
         if (e.work) {
           Raw<2> w;
           pack(p, e.meta.out_dtype() == SPIN4D_BF16, w);
@@ -761,14 +810,16 @@ int norm_launches(const spin4d_grad_tensor* ts, int count, NormArgs f, cudaStrea
       list.at[k] = {t.grad, meta_of(t.n, t.grad_dtype, 0, shift)};
       add_tiles(list.tile0, k, t.n, shift);
     }
-    const int most = std::min(4 * sm_count(), kMaxNormBlocks);
-    // A block that begins another tensor waits for its first values once more, about PAD tiles' time: where
-    // blocks have several tiles, a tensor of a long list counts for that many more.
+    const int most = std::min(kNormBlocks * sm_count(), kMaxNormBlocks);
+    // A block that begins another tensor waits for its first values once more, about kTensorTiles tiles' time:
+    // where blocks have several tiles, a tensor of a long list counts for that many more.  (16.8M fp16 values
+    // and 40 tensors of up to 20000: 22.2 us without, 14.4 with 3, 13.4 with 6; 300 tensors of up to 65536:
+    // 12.0, 9.4 and 9.5.)
     if (CAP > 16 && list.tile0[list.count] > (uint32_t)most) {
       uint32_t more = 0;
       for (int k = 0; k < list.count; ++k) {
         const bool some = list.at[k].meta.n() > 0;
-        if (some) more += PAD;
+        if (some) more += kTensorTiles;
         list.tile0[k + 1] += more;
       }
     }
@@ -785,6 +836,8 @@ int norm_launches(const spin4d_grad_tensor* ts, int count, NormArgs f, cudaStrea
 template <int NORM>
 int norm_list(const spin4d_grad_tensor* ts, int count, const NormArgs& f, cudaStream_t s) {
   if (count <= 16) return norm_launches<16, NORM>(ts, count, f, s);
+  if (count <= 64) return norm_launches<64, NORM>(ts, count, f, s);
+  if (count <= 320) return norm_launches<320, NORM>(ts, count, f, s);
   return norm_launches<kNormCap, NORM>(ts, count, f, s);
 }
 
@@ -803,7 +856,7 @@ int clip_launches(const spin4d_grad_tensor* ts, int count, const spin4d_grad_con
       list.at[k] = {t.grad, out, meta_of(t.n, t.grad_dtype, out_dtype, shift)};
       add_tiles(list.tile0, k, t.n, shift);
     }
-    const int blocks = split(list, CLIP_PER * sm_count());
+    const int blocks = split(list, kClipBlocks * sm_count());
     if (!list.tiles) continue;
     SPIN4D_CHECK(launch(clip_kernel<CAP>, blocks, s, list, control));
   }
@@ -826,7 +879,7 @@ int adam_launches(const spin4d_adam_tensor* ts, int count, const AdamArgs& a, cu
                     t.weight_decay};
       add_tiles(list.tile0, k, t.n, shift);
     }
-    const int blocks = split(list, ADAM_PER * sm_count());
+    const int blocks = split(list, kAdamBlocks * sm_count());
     if (!list.tiles) continue;
     SPIN4D_CHECK(launch(adam_list_kernel<CAP>, blocks, s, list, a));
   }
@@ -897,6 +950,8 @@ extern "C" int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, c
   if (tiles >= (int64_t(1) << 31) || used.clash()) return SPIN4D_ERR_INVALID;
   if (fault_injected("spin4d_clip_grads")) return SPIN4D_ERR_INJECTED;
   if (count <= 16) return clip_launches<16>(tensors, count, control, (cudaStream_t)stream);
+  if (count <= 64) return clip_launches<64>(tensors, count, control, (cudaStream_t)stream);
+  if (count <= 320) return clip_launches<320>(tensors, count, control, (cudaStream_t)stream);
   return clip_launches<1024>(tensors, count, control, (cudaStream_t)stream);
 }
 
@@ -943,5 +998,7 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
   a.control = control;
   a.flag = nonfinite_flag;
   if (count <= 16) return adam_launches<16>(tensors, count, a, (cudaStream_t)stream);
+  if (count <= 64) return adam_launches<64>(tensors, count, a, (cudaStream_t)stream);
+  if (count <= 224) return adam_launches<224>(tensors, count, a, (cudaStream_t)stream);
   return adam_launches<448>(tensors, count, a, (cudaStream_t)stream);
 }

@@ -7,6 +7,7 @@ the library is missing the import fails loudly; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 import struct
 from typing import Dict, Optional, Sequence, Union
@@ -395,39 +396,49 @@ class _TensorList:
 
 
 def _one_device(tensors) -> Optional[torch.device]:
-    dev = None
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("the tensors of a list must be on one device")
-    return dev
+    devices = {t.device for t in tensors}
+    if not devices:
+        return None
+    if any(d.type != "cuda" for d in devices):
+        raise ValueError("tensors must be on a CUDA device")
+    if len(devices) > 1:
+        raise ValueError("the tensors of a list must be on one device")
+    return devices.pop()
 
 
-def _list_dtype(t: torch.Tensor, allowed=(torch.float32, torch.float16, torch.bfloat16)) -> int:
-    if t.dtype not in allowed:
-        raise ValueError("unsupported dtype %s" % t.dtype)
-    return _LIST_DT[t.dtype]
+def _column(tensors, allowed=(torch.float32, torch.float16, torch.bfloat16), optional: bool = False):
+    """(addresses, lengths, types) of one tensor of each row; 0 for None."""
+    if not optional and any(t is None for t in tensors):
+        raise ValueError("only outputs and working copies may be None")
+    if not all(t is None or t.is_contiguous() for t in tensors):
+        raise ValueError("tensor must be contiguous")
+    for dt in {t.dtype for t in tensors if t is not None}:
+        if dt not in allowed:
+            raise ValueError("unsupported dtype %s" % dt)
+    return ([0 if t is None else t.data_ptr() for t in tensors], [None if t is None else t.numel() for t in tensors],
+            [0 if t is None else _LIST_DT[t.dtype] for t in tensors])
+
+
+def _same_lengths(lengths, others, what: str) -> None:
+    for column in others:
+        if column != lengths and any(b is not None and a != b for a, b in zip(lengths, column)):
+            raise ValueError(what)
 
 
 class GradList(_TensorList):
     """Gradients (float32, float16 or bfloat16) for grad_norm and clip_grads,
     with the outputs that clip_grads writes (None: in place)."""
 
-    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[Optional[torch.Tensor]]] = None):
         grads = list(grads)
         outs = [None] * len(grads) if outs is None else list(outs)
         if len(outs) != len(grads):
             raise ValueError("one output for each gradient")
-        values = []
-        for g, o in zip(grads, outs):
-            if o is not None and o.numel() != g.numel():
-                raise ValueError("an output has its gradient's size")
-            values += (_ptr(g) or 0, 0 if o is None else _ptr(o) or 0, g.numel(), _list_dtype(g),
-                       0 if o is None else _list_dtype(o))
-        self._seal(GradTensor, "QQqii", values, grads + [o for o in outs if o is not None], len(grads))
+        g, n, g_dt = _column(grads)
+        o, o_n, o_dt = _column(outs, optional=True)
+        _same_lengths(n, [o_n], "an output has its gradient's size")
+        self._seal(GradTensor, "QQqii", itertools.chain.from_iterable(zip(g, o, n, g_dt, o_dt)),
+                   grads + [t for t in outs if t is not None], len(grads))
 
 
 class AdamList(_TensorList):
@@ -441,16 +452,16 @@ class AdamList(_TensorList):
         rates = [list(x) if isinstance(x, (list, tuple)) else [float(x)] * n for x in (lr, weight_decay)]
         if any(len(x) != n for x in [grads, m, v, work] + rates):
             raise ValueError("one gradient, m, v, rate and working copy for each parameter tensor")
-        values = []
-        for p, g, mm, vv, w, r, d in zip(params, grads, m, v, work, *rates):
-            if any(x is not None and x.numel() != p.numel() for x in (g, mm, vv, w)):
-                raise ValueError("a parameter's gradient, state and working copy have its size")
-            for x in (p, mm, vv):
-                _list_dtype(x, (torch.float32,))
-            values += (_ptr(p) or 0, 0 if w is None else _ptr(w) or 0, _ptr(g) or 0, _ptr(mm) or 0, _ptr(vv) or 0,
-                       p.numel(), r, d, _list_dtype(g),
-                       0 if w is None else _list_dtype(w, (torch.float16, torch.bfloat16)))
-        self._seal(AdamTensor, "QQQQQqffii", values, params + grads + m + v + [w for w in work if w is not None], n)
+        fp32 = (torch.float32,)
+        p_at, size, _ = _column(params, fp32)
+        m_at, m_n, _ = _column(m, fp32)
+        v_at, v_n, _ = _column(v, fp32)
+        g_at, g_n, g_dt = _column(grads)
+        w_at, w_n, w_dt = _column(work, (torch.float16, torch.bfloat16), optional=True)
+        _same_lengths(size, [m_n, v_n, g_n, w_n], "a parameter's gradient, state and working copy have its size")
+        self._seal(AdamTensor, "QQQQQqffii",
+                   itertools.chain.from_iterable(zip(p_at, w_at, g_at, m_at, v_at, size, *rates, g_dt, w_dt)),
+                   params + grads + m + v + [t for t in work if t is not None], n)
 
 
 def grad_list(grads, outs=None) -> GradList:

@@ -13,9 +13,10 @@ off by at most half of that type's step, or half of its smallest subnormal.
     v: the same with g twice rounded and squared: 7u of the (positive) sum;
     1/(1-b^t): t log b rounded (at most u after expm1, whose condition is
        x e^x/(e^x - 1) <= 1 for x < 0), expm1f within 1 ulp = 2u, division u: 4u;
-    mh: m's error and 5u |mh|; sqrt(vh): (7u + 5u)/2 + u = 7u; + eps (rounded u,
-       added u): 9u of the denominator; lr rounded u, product u, quotient u:
-       in all 17u |update| + lr * (5u (|b1 m| + |(1-b1) g|)) / (1-b1^t) / denominator;
+    mh: m's error and 5u |mh|; sqrt(vh), itself within 2^-23 = 2u: (7u + 5u)/2 + 2u
+       = 8u; + eps (rounded u, added u): 10u of the denominator; lr rounded u,
+       product u, quotient within 2 ulp = 4u: in all 21u |update| + lr * (5u (|b1 m| +
+       |(1-b1) g|)) / (1-b1^t) / denominator;
     p: decay * p: lr * decay rounded twice over (lr u, decay u, product u, product u): 4u;
        the sum of both and the difference from p: u of each.
   fp32 subnormals add at most 2^-148 to m and v.
@@ -52,7 +53,7 @@ def adam_bounds(p, g, m, v, step, lr, b1, b2, eps, decay=0.0, coef=1.0):
     with np.errstate(divide="ignore", invalid="ignore"):
         scale = lr / (1 - b1 ** step) / den
         upd = np.where(terms > 0, terms * scale, 0.0)      # no smaller than |update|
-        dp = np.where(terms > 0, (17.1 + 5.05) * U * upd, 0.0)
+        dp = np.where(terms > 0, (21.1 + 5.05) * U * upd, 0.0)
     shrink = lr * decay * p
     dp = dp + 4.05 * U * shrink + U * (upd + shrink) + U * (p + upd + shrink) + TINY
     return dp, dm, dv

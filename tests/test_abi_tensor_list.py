@@ -154,6 +154,10 @@ def test_binding_refuses(sp):
     with pytest.raises(ValueError):
         sp.grad_list([cpu], [torch.zeros(7)])
     with pytest.raises(ValueError):
+        sp.grad_list([None])
+    with pytest.raises(ValueError):
+        sp.adam_list([cpu], [None], [cpu], [cpu], lr=1e-3)
+    with pytest.raises(ValueError):
         sp.adam_list([cpu], [cpu], [cpu], [], lr=1e-3)
     with pytest.raises(ValueError):
         sp.adam_list([cpu], [torch.zeros(7)], [cpu], [cpu], lr=1e-3)
