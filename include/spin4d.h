@@ -309,7 +309,8 @@ typedef struct spin4d_grad_tensor {
 } spin4d_grad_tensor;
 
 /* Device memory of the caller, 16-byte aligned; zeroed before its first use
- * (step: set to the steps already taken when training resumes). */
+ * (step: set to the steps already taken when training resumes).  Calls that
+ * can overlap on the GPU need one each. */
 typedef struct spin4d_grad_control {
     float norm;             /* of grad_scale * gradient over the whole list */
     float coef;             /* clipped gradient = coef * stored gradient */
@@ -330,8 +331,9 @@ size_t spin4d_grad_norm_workspace(int count);
  * fp32 number (a NaN or infinity in any gradient), coef is 0, `step` stays and
  * `skipped` counts it.  norms (optional, `count` fp32 values): each tensor's
  * own norm, likewise scaled.  Squares and sums are 64-bit and are added in an
- * order that depends on the list and the device alone: the same gradients give
- * the same bits.  A tensor listed twice counts twice.
+ * order that the lengths, types and alignments of the list and the device
+ * alone determine: the same gradients give the same bits.  A tensor listed
+ * twice counts twice.
  *   workspace  device, spin4d_grad_norm_workspace(count) bytes, 256-byte
  *              aligned, contents ignored on entry; calls that can overlap on
  *              the GPU (other streams, captured graphs) need one each
@@ -373,8 +375,9 @@ typedef struct spin4d_adam_tensor {
  *   m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2;
  *   p -= lr * (m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps) + lr * weight_decay * p
  * t = step when step > 0, else control->step (which spin4d_grad_norm has
- * advanced).  Where control->norm is not finite (or t < 1) params, params_work,
- * m and v stay as they are.  zero_grad != 0 clears the gradients in either
+ * advanced).  The square root is within 2^-23 of itself and the quotient within
+ * 2 ulp.  Where control->norm is not finite (or t < 1) params, params_work, m
+ * and v stay as they are.  zero_grad != 0 clears the gradients in either
  * case.  nonfinite_flag as in spin4d_adam_step.  SPIN4D_ERR_INVALID when an
  * array that is written overlaps another one of the list; gradients that are
  * not cleared may be shared.

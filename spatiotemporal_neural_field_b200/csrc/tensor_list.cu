@@ -86,16 +86,25 @@ struct List {
   int count;
   uint32_t tiles;
   uint32_t per;                               // tiles of a block
-  uint32_t hint_shift;                        // hint[t >> hint_shift]: a tensor at or before the tile's owner
+  uint32_t hint_shift;
   uint32_t tile0[CAP + 1];
-  uint16_t hint[CAP > 16 ? kHints : 2];
+  uint16_t hint[CAP > 16 ? kHints + 1 : 2];   // the owner of each 2^hint_shift-th tile, and the last tensor
   Entry at[CAP];
 
   // The last tensor that begins at or before the tile: its owner (tensors without values own none).
   __device__ __forceinline__ int owner(uint32_t tile) const {
-    int k = CAP > 16 ? hint[tile >> hint_shift] : 0;
-    while (k + 1 < count && tile0[k + 1] <= tile) ++k;
-    return k;
+    if (CAP <= 16) {
+      int k = 0;
+      while (k + 1 < count && tile0[k + 1] <= tile) ++k;
+      return k;
+    }
+    int lo = hint[tile >> hint_shift], hi = hint[(tile >> hint_shift) + 1] + 1;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tile0[mid] <= tile) lo = mid;
+      else hi = mid;
+    }
+    return lo;
   }
 };
 
@@ -771,7 +780,7 @@ int split(List<Entry, CAP>& list, int most) {
   if (CAP > 16) {
     while ((list.tiles >> list.hint_shift) >= (uint32_t)kHints) ++list.hint_shift;
     int k = 0;
-    for (int h = 0; h < kHints; ++h) {
+    for (int h = 0; h <= kHints; ++h) {
       const uint64_t tile = (uint64_t)h << list.hint_shift;
       while (k + 1 < list.count && list.tile0[k + 1] <= tile) ++k;
       list.hint[h] = (uint16_t)k;

@@ -80,6 +80,31 @@ def test_norm_of_many_tensors(sp, count):
     tt.within(host(norms), each, tt.scalar_bound(np.array(each)), "norms")
 
 
+@pytest.mark.parametrize("kind", ["l2", "l1", "inf"])
+@pytest.mark.parametrize("big_at", [0, 60, 120])
+def test_norms_of_long_and_short_tensors_of_every_type(sp, big_at, kind):
+    """A tensor of many blocks among 120 of a few values, types mixed: the parts of each are kept apart."""
+    lens = [int(x) for x in np.random.default_rng(4).integers(0, 5000, 120)]
+    lens[3] = lens[70] = 0
+    lens.insert(big_at, 3_000_001)
+    views = []
+    for k, n in enumerate(lens):
+        t = list(TYPES)[k % 3]
+        views.append(packed([n], t, 200 + k, scale=10.0 ** -(k % 5), gap=1 + k % 4)[0][0])
+    ctl, norms = sp.grad_control(), torch.full((len(lens),), -1.0, device="cuda")
+    want, coef, each = tl.grad_norm([host(v) for v in views], max_norm=0.5, kind=kind)
+    for given in (norms, None):
+        sp.grad_norm(views, ctl, max_norm=0.5, norm_type=kind, norms=given)
+        tt.within(host(ctl.norm), want, tt.scalar_bound(want), "norm")
+        tt.within(host(ctl.coef), coef, tt.scalar_bound(coef), "coef")
+    tt.within(host(norms), each, tt.scalar_bound(np.array(each)), "norms")
+    old = [host(v) for v in views]
+    sp.clip_grads(views, ctl)
+    for k, (v, o) in enumerate(zip(views, old)):
+        w = tl.clip(o, float(ctl.coef))
+        tt.within(host(v), w, tt.clip_bound(w, list(TYPES)[k % 3]), "clip of %d" % lens[k])
+
+
 @pytest.mark.parametrize("n", [16_777_216 + 6987, 134_217_728 + 3])
 def test_norm_of_long_tensors_is_deterministic(sp, n):
     g = torch.randn(n, device="cuda", generator=gen(3))
@@ -371,6 +396,38 @@ def test_captured_sequence_replays_as_the_eager_one(sp, count):
         assert int(eager[4].step) == (i + 1 if i < 2 else i) and int(eager[4].skipped) == (i >= 2)
         for k in (0, 1, 2, 3, 4):
             assert torch.equal(eager[1][k], graphed[1][k])
+
+
+def test_captured_across_streams(sp):
+    """Gradients written on two streams, joined, measured and used on a third: in a graph, replayed."""
+    n = 50_001
+    g = [torch.zeros(n, device="cuda") for _ in range(2)]
+    src = [torch.randn(n, device="cuda", generator=gen(90 + k)) for k in range(2)]
+    p, m, v = ([torch.zeros(n, device="cuda") for _ in range(2)] for _ in range(3))
+    ctl, ws = sp.grad_control(), torch.empty(sp.grad_norm_workspace(2), dtype=torch.uint8, device="cuda")
+    grads, adam = sp.grad_list(g), sp.adam_list(p, g, m, v, lr=1e-2)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=streams[2]):
+        for k in range(2):
+            streams[k].wait_stream(streams[2])
+            with torch.cuda.stream(streams[k]):
+                g[k].add_(src[k])
+            streams[2].wait_stream(streams[k])
+        sp.grad_norm(grads, ctl, max_norm=1.0, workspace=ws)
+        sp.adam_step_tensors(adam, 0.9, 0.99, 1e-8, control=ctl, zero_grad=True)
+    for i in range(3):
+        old = [[host(x[k]) for x in (p, src, m, v)] for k in range(2)]
+        graph.replay()
+        torch.cuda.synchronize()
+        want, coef, _ = tl.grad_norm([o[1] for o in old], max_norm=1.0)
+        tt.within(host(ctl.norm), want, tt.scalar_bound(want), "norm")
+        h = dict(step=i + 1, lr=1e-2, b1=0.9, b2=0.99, eps=1e-8, coef=float(ctl.coef))
+        for k in range(2):
+            for name, got, w, b in zip("pmv", (p[k], m[k], v[k]), tl.adamw_step(*old[k], **h), tt.adam_bounds(*old[k], **h)):
+                tt.within(host(got), w, b, "%s of replay %d" % (name, i))
+    assert int(ctl.step) == 3
 
 
 def test_two_streams_at_once(sp):
