@@ -35,9 +35,9 @@ constexpr int kMaxTensors = 1 << 16;
 // Blocks of a launch, at most, for each SM.  The norm's are all resident at once (64 registers a thread), each
 // writes slots that one block adds in the end.  Clip and Adam meet nowhere: short blocks that the hardware hands
 // out as others end keep loads and stores mixed and both dies busy.  Adam over 134M parameters: 669 us with 3
-// a SM (all resident), 618 with 32, 602 with 64, 595 with 128; clip of 16.8M fp16 into fp32 with its norm:
-// 36.0 us with 4, 29.7 with 8, 30.2 with 12, 31.2 with 32, 35.6 with 64.
-constexpr int kNormBlocks = 4, kClipBlocks = 8, kAdamBlocks = 96;
+// a SM (all resident), 618 with 32, 602 with 64, 595 with 128; norm and clip of 16.8M fp16 values into fp32:
+// 36.0 us with 4, 27.5 with 8, 26.4 with 32, 30.8 with 64; of 11.5M fp32: 25.5, 25.0, 23.6 and 23.1.
+constexpr int kNormBlocks = 4, kClipBlocks = 32, kAdamBlocks = 96;
 // Tiles that a tensor of a long list counts for besides its own (see norm_launches).
 constexpr uint32_t kTensorTiles = 4;
 
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
 // Tiles [t, stop) of one tensor, from the last down.
 template <int BYTES>
 __device__ __forceinline__ void clip_tiles(const void* a, void* o, const Meta meta, uint32_t t, uint32_t stop, float coef) {
-  constexpr int kAhead = 8 / BYTES;           // 16 registers of loads in flight
+  constexpr int kAhead = 4 / BYTES;           // 8 registers of loads in flight; the blocks are many
   const int64_t n = meta.n();
   const int shift = meta.shift();
   while (stop > t) {
@@ -683,86 +683,71 @@ __global__ void __launch_bounds__(kThreads, 3) adam_list_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 bool dtype_ok(int dt) { return dt == SPIN4D_F32 || dt == SPIN4D_F16 || dt == SPIN4D_BF16; }
 
-bool array_ok(const void* p, int64_t n, int bytes) { return n == 0 || (p && aligned(p, bytes)); }
+bool array_ok(const void* p, int64_t n, int bytes) { return n == 0 || (p && ((uintptr_t)p & (bytes - 1)) == 0); }
 
-// The stretches of memory that a call reads or writes, family by family (all parameters, all gradients, ...).
-// A family is nearly always in the order of its addresses and apart from the others; only what is not gets
-// sorted or merged.  `ok` is false when the host has no memory for a long list.
-class Stretches {
- public:
-  Stretches(int families, int count) : families_(families), count_(count) {
-    at_ = families * count <= kLocal ? local_ : new (std::nothrow) Stretch[(size_t)families * count];
-  }
-  ~Stretches() {
-    if (at_ != local_) delete[] at_;
-  }
-  Stretches(const Stretches&) = delete;
-  Stretches& operator=(const Stretches&) = delete;
-  bool ok() const { return at_ != nullptr; }
-
-  void add(int family, bool write, const void* p, int64_t n, int bytes) {
-    if (!p || n == 0) return;
-    Family& f = family_[family];
-    const uintptr_t lo = (uintptr_t)p, hi = lo + (uint64_t)n * bytes;
-    f.write = write;
-    f.ordered = f.ordered && lo >= f.hi;
-    f.lo = f.count ? std::min(f.lo, lo) : lo;
-    f.hi = std::max(f.hi, hi);
-    at_[(size_t)family * count_ + f.count++] = {lo, hi};
-  }
-
-  // Whether something written is also another array's: blocks run in no order, so the result would have none.
-  bool clash() {
-    int order[kFamilies], used = 0;
-    for (int i = 0; i < families_; ++i) {
-      Family& f = family_[i];
-      if (!f.count) continue;
-      order[used++] = i;
-      if (f.ordered) continue;
-      Stretch* at = at_ + (size_t)i * count_;
-      std::sort(at, at + f.count, [](const Stretch& a, const Stretch& b) { return a.lo < b.lo; });
-      if (f.write)
-        for (int k = 1; k < f.count; ++k)
-          if (at[k].lo < at[k - 1].hi) return true;
-    }
-    std::sort(order, order + used, [this](int a, int b) { return family_[a].lo < family_[b].lo; });
-    bool apart = true;
-    for (int i = 1; i < used; ++i) apart = apart && family_[order[i]].lo >= family_[order[i - 1]].hi;
-    if (apart) return false;
-    // all of them in the order of their addresses
-    int next[kFamilies] = {};
-    uintptr_t any = 0, written = 0;
-    for (;;) {
-      int best = -1;
-      for (int i = 0; i < used; ++i) {
-        const int f = order[i];
-        if (next[f] < family_[f].count && (best < 0 || head(f, next).lo < head(best, next).lo)) best = f;
-      }
-      if (best < 0) return false;
-      const Stretch s = head(best, next);
-      ++next[best];
-      if (s.lo < (family_[best].write ? any : written)) return true;
-      any = std::max(any, s.hi);
-      if (family_[best].write) written = std::max(written, s.hi);
-    }
-  }
-
- private:
-  static constexpr int kLocal = 320, kFamilies = 5;
-  struct Stretch {
-    uintptr_t lo, hi;
-  };
-  struct Family {
-    int count = 0;
-    bool write = false, ordered = true;       // ordered: each begins where the last ended, or behind
-    uintptr_t lo = 0, hi = 0;
-  };
-  const Stretch& head(int family, const int* next) const { return at_[(size_t)family * count_ + next[family]]; }
-  int families_, count_;
-  Family family_[kFamilies];
-  Stretch local_[kLocal];
-  Stretch* at_;
+// A stretch of memory that a call reads or writes.
+struct Stretch {
+  uintptr_t lo = 0, hi = 0;
+  bool write = false;
+  Stretch() = default;
+  Stretch(const void* p, int64_t n, int bytes, bool write_)
+      : lo(p ? (uintptr_t)p : 0), hi(p ? (uintptr_t)p + (uint64_t)n * bytes : 0), write(write_) {}
+  bool empty() const { return lo == hi; }
 };
+
+// Whether something that a call writes is also another array's: blocks run in no order, so the result would have
+// none.  get(k, f) is the stretch of tensor k in family f (its parameters, its gradient, ...).  Families are
+// nearly always in the order of their addresses and apart from one another, which one look over them shows;
+// else all stretches are sorted.  True also when the host has no memory for that.
+template <int FAMILIES, typename Get>
+bool clash(int count, Get get) {
+  Stretch box[FAMILIES];
+  bool apart = true;
+  for (int k = 0; k < count; ++k)
+#pragma GCC unroll 5
+    for (int f = 0; f < FAMILIES; ++f) {
+      const Stretch s = get(k, f);
+      if (s.empty()) continue;
+      if (box[f].empty()) {
+        box[f] = s;
+      } else {
+        apart = apart && s.lo >= box[f].hi;
+        box[f].lo = std::min(box[f].lo, s.lo);
+        box[f].hi = std::max(box[f].hi, s.hi);
+      }
+    }
+  const auto before = [](const Stretch& a, const Stretch& b) { return a.lo < b.lo; };
+  if (apart) {
+    std::sort(box, box + FAMILIES, before);
+    uintptr_t any = 0;
+    for (const Stretch& s : box) {
+      if (s.empty()) continue;
+      apart = apart && s.lo >= any;
+      any = s.hi;
+    }
+    if (apart) return false;
+  }
+  Stretch local[320];
+  const size_t most = (size_t)FAMILIES * count;
+  Stretch* const at = most <= 320 ? local : new (std::nothrow) Stretch[most];
+  if (!at) return true;
+  int used = 0;
+  for (int k = 0; k < count; ++k)
+    for (int f = 0; f < FAMILIES; ++f) {
+      const Stretch s = get(k, f);
+      if (!s.empty()) at[used++] = s;
+    }
+  std::sort(at, at + used, before);
+  uintptr_t any = 0, written = 0;
+  bool found = false;
+  for (int i = 0; i < used && !found; ++i) {
+    found = at[i].lo < (at[i].write ? any : written);
+    any = std::max(any, at[i].hi);
+    if (at[i].write) written = std::max(written, at[i].hi);
+  }
+  if (at != local) delete[] at;
+  return found;
+}
 
 int shift_of(const void* p, int bytes) { return (int)(((uintptr_t)p & (kVec * bytes - 1)) / bytes); }
 
@@ -939,8 +924,6 @@ extern "C" int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, c
                                  spin4d_stream_t stream) {
   if (count < 0 || count > kMaxTensors || (count > 0 && !tensors)) return SPIN4D_ERR_INVALID;
   if (!control || !aligned(control, 16)) return SPIN4D_ERR_INVALID;
-  Stretches used(2, count);
-  if (!used.ok()) return SPIN4D_ERR_INVALID;
   int64_t tiles = 0;
   for (int k = 0; k < count; ++k) {
     const spin4d_grad_tensor& t = tensors[k];
@@ -948,15 +931,16 @@ extern "C" int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, c
       return SPIN4D_ERR_INVALID;
     if (!array_ok(t.grad, t.n, dtype_bytes(t.grad_dtype))) return SPIN4D_ERR_INVALID;
     if (t.out && !array_ok(t.out, t.n, dtype_bytes(t.out_dtype))) return SPIN4D_ERR_INVALID;
-    if (!t.out || (t.out == t.grad && t.out_dtype == t.grad_dtype)) {
-      used.add(0, true, t.grad, t.n, dtype_bytes(t.grad_dtype));
-    } else {
-      used.add(1, false, t.grad, t.n, dtype_bytes(t.grad_dtype));
-      used.add(0, true, t.out, t.n, dtype_bytes(t.out_dtype));
-    }
     tiles += t.n / kTile + 2;
   }
-  if (tiles >= (int64_t(1) << 31) || used.clash()) return SPIN4D_ERR_INVALID;
+  if (tiles >= (int64_t(1) << 31)) return SPIN4D_ERR_INVALID;
+  const auto stretch = [tensors](int k, int f) {
+    const spin4d_grad_tensor& t = tensors[k];
+    const bool in_place = !t.out || (t.out == t.grad && t.out_dtype == t.grad_dtype);
+    if (f == 0) return Stretch(t.grad, t.n, dtype_bytes(t.grad_dtype), in_place);
+    return in_place ? Stretch() : Stretch(t.out, t.n, dtype_bytes(t.out_dtype), true);
+  };
+  if (clash<2>(count, stretch)) return SPIN4D_ERR_INVALID;
   if (fault_injected("spin4d_clip_grads")) return SPIN4D_ERR_INJECTED;
   if (count <= 16) return clip_launches<16>(tensors, count, control, (cudaStream_t)stream);
   if (count <= 64) return clip_launches<64>(tensors, count, control, (cudaStream_t)stream);
@@ -973,26 +957,30 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
   if (!(b1 >= 0.0 && (float)b1 < 1.0f && b2 >= 0.0 && (float)b2 < 1.0f && eps >= 0.0 && isfinite((float)eps)))
     return SPIN4D_ERR_INVALID;
   if ((control && !aligned(control, 16)) || (nonfinite_flag && !aligned(nonfinite_flag, 4))) return SPIN4D_ERR_INVALID;
-  Stretches used(5, count);
-  if (!used.ok()) return SPIN4D_ERR_INVALID;
   int64_t tiles = 0;
   for (int k = 0; k < count; ++k) {
     const spin4d_adam_tensor& t = tensors[k];
     if (t.n < 0 || t.n > kMaxValues || !isfinite(t.lr) || !isfinite(t.weight_decay)) return SPIN4D_ERR_INVALID;
     if (!dtype_ok(t.grad_dtype)) return SPIN4D_ERR_INVALID;
-    if (t.params_work && ((t.work_dtype != SPIN4D_F16 && t.work_dtype != SPIN4D_BF16) || !aligned(t.params_work, 2)))
+    if (t.params_work && ((t.work_dtype != SPIN4D_F16 && t.work_dtype != SPIN4D_BF16) || !array_ok(t.params_work, 1, 2)))
       return SPIN4D_ERR_INVALID;
     if (!array_ok(t.params, t.n, 4) || !array_ok(t.m, t.n, 4) || !array_ok(t.v, t.n, 4) ||
         !array_ok(t.grad, t.n, dtype_bytes(t.grad_dtype)))
       return SPIN4D_ERR_INVALID;
-    used.add(0, true, t.params, t.n, 4);
-    used.add(1, true, t.m, t.n, 4);
-    used.add(2, true, t.v, t.n, 4);
-    used.add(3, true, t.params_work, t.n, 2);
-    used.add(4, zero_grad != 0, t.grad, t.n, dtype_bytes(t.grad_dtype));
     tiles += t.n / kTile + 2;
   }
-  if (tiles >= (int64_t(1) << 31) || used.clash()) return SPIN4D_ERR_INVALID;
+  if (tiles >= (int64_t(1) << 31)) return SPIN4D_ERR_INVALID;
+  const auto stretch = [tensors, zero_grad](int k, int f) {
+    const spin4d_adam_tensor& t = tensors[k];
+    switch (f) {
+      case 0: return Stretch(t.params, t.n, 4, true);
+      case 1: return Stretch(t.m, t.n, 4, true);
+      case 2: return Stretch(t.v, t.n, 4, true);
+      case 3: return Stretch(t.params_work, t.n, 2, true);
+      default: return Stretch(t.grad, t.n, dtype_bytes(t.grad_dtype), zero_grad != 0);
+    }
+  };
+  if (clash<5>(count, stretch)) return SPIN4D_ERR_INVALID;
   if (fault_injected("spin4d_adam_step_tensors")) return SPIN4D_ERR_INJECTED;
   AdamArgs a;
   a.b1 = (float)b1;
