@@ -27,19 +27,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                       // values a thread takes of a tile
 constexpr int kTile = kThreads * kVec;
-constexpr int kMaxNormBlocks = 640;           // the norm's workspace does not depend on the device
+constexpr int kMaxNormBlocks = 480;           // the norm's workspace does not depend on the device
 constexpr int kNormCap = 1024;                // tensors of one launch; longer lists take several
 constexpr int64_t kMaxValues = int64_t(1) << 40;
 constexpr int kMaxTensors = 1 << 16;
 
-// Blocks of a launch, at most, for each SM.  The norm's are all resident at once (64 registers a thread), each
-// writes slots that one block adds in the end.  Clip and Adam meet nowhere: short blocks that the hardware hands
+// Blocks of a launch, at most, for each SM.  The norm's are all resident at once, each writes slots that one block
+// adds in the end: with 2, 3, 4 and 5 a SM the norm of 134M fp16 values takes 49.3, 44.8, 46.8 and 46.7 us, of 300
+// small tensors 8.0, 7.2, 8.6 and 10.8.  Clip and Adam meet nowhere: short blocks that the hardware hands
 // out as others end keep loads and stores mixed and both dies busy.  Adam over 134M parameters: 669 us with 3
 // a SM (all resident), 618 with 32, 602 with 64, 595 with 128; norm and clip of 16.8M fp16 values into fp32:
 // 36.0 us with 4, 27.5 with 8, 26.4 with 32, 30.8 with 64; of 11.5M fp32: 25.5, 25.0, 23.6 and 23.1.
-constexpr int kNormBlocks = 4, kClipBlocks = 32, kAdamBlocks = 96;
+constexpr int kNormBlocks = 3, kClipBlocks = 32, kAdamBlocks = 96;
 // Tiles that a tensor of a long list counts for besides its own (see norm_launches).
-constexpr uint32_t kTensorTiles = 4;
+constexpr uint32_t kTensorTiles = 6;
 
 __host__ __device__ inline int dtype_bytes(int dt) { return dt == SPIN4D_F32 ? 4 : 2; }
 
@@ -366,7 +367,7 @@ __device__ __forceinline__ const T* as_memory(const T* p) {
 }
 
 template <int CAP, int NORM>
-__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ List<NormEntry, CAP> list,
+__global__ void __launch_bounds__(kThreads, kNormBlocks) norm_kernel(const __grid_constant__ List<NormEntry, CAP> list,
                                                            const NormArgs f) {
   __shared__ double part[kParts][kWarps];
   __shared__ int part_slot[kParts];
@@ -657,7 +658,10 @@ __global__ void __launch_bounds__(kThreads, 3) adam_list_kernel(const __grid_con
           const float mh = m[i] * inv_bc1, vh = v[i] * inv_bc2;
           // outside [0, n) all four are 0: with eps = 0 the quotient is NaN there, which neither is stored nor flagged
           p[i] -= __fdividef(lr * mh, root(vh) + a.eps) + decay * p[i];
-          bad |= !isfinite(p[i]) && (q.whole || q.has(i));
+        }
+        if (a.flag) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) bad |= !isfinite(p[i]) && (q.whole || q.has(i));
         }
         put<kKeep>(e.p, SPIN4D_F32, q, p);
         put<kKeep>(e.m, SPIN4D_F32, q, m);
@@ -704,7 +708,6 @@ bool clash(int count, Get get) {
   Stretch box[FAMILIES];
   bool apart = true;
   for (int k = 0; k < count; ++k)
-#pragma GCC unroll 5
     for (int f = 0; f < FAMILIES; ++f) {
       const Stretch s = get(k, f);
       if (s.empty()) continue;
@@ -807,8 +810,8 @@ int norm_launches(const spin4d_grad_tensor* ts, int count, NormArgs f, cudaStrea
     const int most = std::min(kNormBlocks * sm_count(), kMaxNormBlocks);
     // A block that begins another tensor waits for its first values once more, about kTensorTiles tiles' time:
     // where blocks have several tiles, a tensor of a long list counts for that many more.  (16.8M fp16 values
-    // and 40 tensors of up to 20000: 22.2 us without, 14.4 with 3, 13.4 with 6; 300 tensors of up to 65536:
-    // 12.0, 9.4 and 9.5.)
+    // and 40 tensors of up to 20000: 12.5 us with 4, 11.6 with 6; 33M fp32 and 300 of them 25.1 and 24.7.  With
+    // 4 blocks a SM and a longer finish it was 22.2 us without, 14.4 with 3.)
     if (CAP > 16 && list.tile0[list.count] > (uint32_t)most) {
       uint32_t more = 0;
       for (int k = 0; k < list.count; ++k) {
