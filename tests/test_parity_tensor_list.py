@@ -1,5 +1,9 @@
 """GPU parity of the tensor-list calls (global gradient norm, clipping, Adam
 with decoupled weight decay) with the fp64 oracle, through the binding."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -12,6 +16,7 @@ from tests import tol
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 # lengths around a thread's 8 values, a warp's 256 and a tile's 2048
 EDGES = [0, 1, 2, 7, 8, 9, 0, 31, 255, 256, 257, 2039, 2040, 2041, 2047, 2048, 2049, 4096, 6987, 100003]
@@ -470,6 +475,37 @@ def test_offsets_past_32_bits(sp):
     w = np.arange(1.0, 7.0) * float(ctl.coef)
     tt.within(host(g[places]), w, tt.clip_bound(w, "f16"), "clip")
     assert int(torch.count_nonzero(g[:1 << 31])) == 2 and int(torch.count_nonzero(g[1 << 31:])) == 4
+
+
+def test_checked_build_gives_the_same_bits():
+    """Norm, clip and update in the build with device checks, in processes of their own."""
+    code = r"""
+import sys
+sys.path.insert(0, %r)
+import torch
+from spatiotemporal_neural_field_b200 import spin4d as sp
+gen = torch.Generator(device="cuda").manual_seed(1)
+r = lambda n: torch.randn(n, device="cuda", generator=gen)
+g, p, m, v = ([r(n) for n in (70001, 0, 9)] for _ in range(4))
+v = [x.square() for x in v]
+ctl = sp.grad_control()
+sp.grad_norm(g, ctl, max_norm=1.0)
+sp.adam_step_tensors(sp.adam_list(p, g, m, v, lr=1e-2), 0.9, 0.99, 1e-8, control=ctl)
+sp.clip_grads(g, ctl)
+torch.cuda.synchronize()
+sp.check_device_errors(clear=False)
+out = torch.cat([x.view(torch.int32) for x in g + p + m + v] + [ctl.buf]).long()
+print("BITS", sp.lib.spin4d_checked_build(), int((out * torch.arange(1, out.numel() + 1, device="cuda")).sum()))
+""" % ROOT
+    seen = {}
+    for flag in ("0", "1"):
+        r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, SPIN4D_CHECKED=flag), cwd=ROOT,
+                           capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stderr[-3000:]
+        _, checked, bits = r.stdout.split()
+        assert checked == flag
+        seen[flag] = bits
+    assert seen["0"] == seen["1"]
 
 
 def test_a_decoder_trains_through_them(sp):
