@@ -717,21 +717,17 @@ struct Stretch {
 // else all stretches are sorted.  True also when the host has no memory for that.
 template <int FAMILIES, typename Get>
 bool clash(int count, Get get) {
-  Stretch box[FAMILIES];
+  const auto before = [](const Stretch& a, const Stretch& b) { return a.lo < b.lo; };
+  Stretch box[FAMILIES];                      // what a family spans so far
   bool apart = true;
-  for (int k = 0; k < count; ++k)
+  for (int k = 0; k < count && apart; ++k)
     for (int f = 0; f < FAMILIES; ++f) {
       const Stretch s = get(k, f);
       if (s.empty()) continue;
-      if (box[f].empty()) {
-        box[f] = s;
-      } else {
-        apart = apart && s.lo >= box[f].hi;
-        box[f].lo = std::min(box[f].lo, s.lo);
-        box[f].hi = std::max(box[f].hi, s.hi);
-      }
+      if (box[f].hi == 0) box[f].lo = s.lo;
+      apart = apart && s.lo >= box[f].hi;
+      box[f].hi = s.hi;
     }
-  const auto before = [](const Stretch& a, const Stretch& b) { return a.lo < b.lo; };
   if (apart) {
     std::sort(box, box + FAMILIES, before);
     uintptr_t any = 0;
@@ -764,11 +760,11 @@ bool clash(int count, Get get) {
   return found;
 }
 
-int shift_of(const void* p, int bytes) { return (int)(((uintptr_t)p & (kVec * bytes - 1)) / bytes); }
+int shift_of(const void* p, int bytes) { return (int)(((uintptr_t)p & (kVec * bytes - 1)) >> (bytes == 4 ? 2 : 1)); }
 
 // Appends a tensor's tiles; the callers have checked that a list's sum fits.
 void add_tiles(uint32_t* tile0, int k, int64_t n, int shift) {
-  tile0[k + 1] = tile0[k] + (n == 0 ? 0u : (uint32_t)((n + (shift == kStrided ? 0 : shift) + kTile - 1) / kTile));
+  tile0[k + 1] = tile0[k] + (n == 0 ? 0u : (uint32_t)((uint64_t)(n + (shift == kStrided ? 0 : shift) + kTile - 1) / kTile));
 }
 
 // Splits the list over at most `most` blocks; returns how many.

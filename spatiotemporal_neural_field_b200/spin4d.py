@@ -504,27 +504,28 @@ def grad_norm_workspace(count: int) -> int:
     return int(lib.spin4d_grad_norm_workspace(count))
 
 
-def _on_device(index: int, t: torch.Tensor, what: str) -> int:
-    if t.get_device() != index:
-        raise ValueError("%s must be on the list's device" % what)
-    return _ptr(t)
-
-
 # torch.cuda.current_stream and current_device build objects; these give the numbers
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _list_call(name: str, function, index: int, stream, *args) -> None:
-    """The call on the list's device, on the given stream or the device's current one."""
-    if _current_device() == index:
-        status = function(*args, _raw_stream(index) if stream is None else _stream(stream))
+def _list_call(name: str, index: int, stream, args) -> None:
+    """A tensor-list call on the list's device, on the given stream or the
+    device's current one (short lists are bound by the host, so the usual
+    case comes first)."""
+    if stream is None and _current_device() == index:
+        status = getattr(lib, name)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = function(*args, _raw_stream(index) if stream is None else _stream(stream))
+            status = getattr(lib, name)(*args, _raw_stream(index) if stream is None else _stream(stream))
     if status != OK:
         raise Spin4dError(name, status)
+
+
+def _same_device(grads, control) -> None:
+    if grads.index != control.index and grads.index is not None:
+        raise ValueError("the control block must be on the list's device")
 
 
 def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_type: str = "l2",
@@ -541,21 +542,24 @@ def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_
     kind = _NORMS.get(norm_type)
     if kind is None:
         raise ValueError("norm_type must be one of %s" % (sorted(_NORMS),))
+    _same_device(grads, control)
     index = control.index
-    if grads.index is not None and grads.index != index:
-        raise ValueError("the control block must be on the list's device")
+    norms_at = None
     if norms is not None:
-        if norms.dtype != torch.float32 or norms.numel() != grads.count:
-            raise ValueError("norms: one float32 value for each tensor")
-        norms = _on_device(index, norms, "norms") or None
+        if (norms.dtype != torch.float32 or norms.numel() != grads.count or norms.get_device() != index
+                or not norms.is_contiguous()):
+            raise ValueError("norms: one contiguous float32 value for each tensor, on the list's device")
+        norms_at = norms.data_ptr() or None
     if workspace is None:
         workspace = torch.empty(grad_norm_workspace(grads.count), dtype=torch.uint8, device=control.device)
         if stream is not None:      # the allocator must not hand it on before that stream is done with it
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                     else torch.cuda.ExternalStream(_stream(stream), control.device))
-    _list_call("spin4d_grad_norm", lib.spin4d_grad_norm, index, stream, grads.address, grads.count, kind, grad_scale,
-               max_norm, control.address, norms, _on_device(index, workspace, "the workspace"),
-               workspace.numel() * workspace.element_size())
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous, on the list's device")
+    _list_call("spin4d_grad_norm", index, stream,
+               (grads.address, grads.count, kind, grad_scale, max_norm, control.address, norms_at,
+                workspace.data_ptr(), workspace.nbytes))
     return control
 
 
@@ -564,10 +568,8 @@ def clip_grads(grads, control: GradControl, stream=None) -> None:
     list's outputs; a coefficient of 0 writes zeros."""
     if type(grads) is not GradList:
         grads = GradList(grads)
-    if grads.index is not None and grads.index != control.index:
-        raise ValueError("the control block must be on the list's device")
-    _list_call("spin4d_clip_grads", lib.spin4d_clip_grads, control.index, stream, grads.address, grads.count,
-               control.address)
+    _same_device(grads, control)
+    _list_call("spin4d_clip_grads", control.index, stream, (grads.address, grads.count, control.address))
 
 
 def adam_step_tensors(tensors: AdamList, b1: float, b2: float, eps: float, step: int = 0,
@@ -580,12 +582,16 @@ def adam_step_tensors(tensors: AdamList, b1: float, b2: float, eps: float, step:
     index = tensors.index
     if index is None:
         return
-    if control is not None and control.index != index:
-        raise ValueError("the control block must be on the list's device")
+    control_at = flag_at = None
+    if control is not None:
+        _same_device(tensors, control)
+        control_at = control.address
     if nonfinite_flag is not None:
-        nonfinite_flag = _on_device(index, nonfinite_flag, "the flag")
-    _list_call("spin4d_adam_step_tensors", lib.spin4d_adam_step_tensors, index, stream, tensors.address, tensors.count,
-               step, b1, b2, eps, 1 if zero_grad else 0, None if control is None else control.address, nonfinite_flag)
+        if nonfinite_flag.get_device() != index or nonfinite_flag.dtype != torch.int32:
+            raise ValueError("the flag: an int32 value on the list's device")
+        flag_at = nonfinite_flag.data_ptr()
+    _list_call("spin4d_adam_step_tensors", index, stream,
+               (tensors.address, tensors.count, step, b1, b2, eps, 1 if zero_grad else 0, control_at, flag_at))
 
 
 # ---- the paper's four-head decoder ----
