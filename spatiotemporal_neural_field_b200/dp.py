@@ -38,7 +38,10 @@ def max_over_ranks(value: float, device=None) -> float:
 
 
 def allreduce_gradients(tensors: Iterable[torch.Tensor]) -> None:
-    """Sum gradient tensors over ranks in place (before a replicated Adam)."""
+    """Sum gradient tensors over ranks in place (before a replicated Adam).
+    ``spin4d.grad_norm(..., grad_scale=1 / world())`` turns the sum into a mean
+    on the way to the update; the gradients being the same on every rank, so is
+    their norm."""
     if world() == 1:
         return
     for t in tensors:
