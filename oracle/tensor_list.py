@@ -30,7 +30,7 @@ def grad_norm(grads, max_norm: float = np.inf, kind: str = "l2", scale: float = 
         norm = float(np.sum(each))
     else:
         norm = float(np.max(each)) if each else 0.0
-    if not np.isfinite(norm) or norm > np.finfo(np.float32).max:
+    if not np.isfinite(norm) or norm > float(np.finfo(np.float32).max):
         return norm, 0.0, each
     return norm, scale * min(1.0, max_norm / (norm + CLIP_EPS)), each
 

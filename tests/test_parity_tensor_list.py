@@ -133,7 +133,7 @@ def test_norm_over_the_whole_range_of_fp32(sp):
                 ctl = sp.grad_control()
                 sp.grad_norm([g], ctl, max_norm=1.0, grad_scale=scale)
                 want, coef, _ = tl.grad_norm([np.full(n, v)], max_norm=1.0, scale=scale)
-                if want > np.finfo(np.float32).max:         # not a number of fp32: treated as infinite
+                if want > float(np.finfo(np.float32).max):         # not a number of fp32: treated as infinite
                     assert torch.isinf(ctl.norm) and float(ctl.coef) == 0 and int(ctl.skipped) == 1
                     continue
                 tt.within(host(ctl.norm), want, tt.scalar_bound(want), "norm of %g" % value)
@@ -350,6 +350,52 @@ def test_entries_without_gradient_stay(sp):
     args = (host(q), host(g), np.zeros(2049), np.zeros(2049))
     h = dict(step=1, lr=2.0 ** -6, b1=0.0, b2=0.0, eps=0.0)
     tt.within(host(p), host(q) - 2.0 ** -6, tt.adam_bounds(*args, **h)[0], "g / sqrt(g^2) = 1")
+
+
+@pytest.mark.parametrize("work", [None, "bf16"])
+def test_updates_over_the_range_of_gradients(sp, work):
+    """From parameters of zero, so that nothing hides the update: gradients from 1e-25 (whose squares vanish next
+    to eps) to 1e15."""
+    n = 200_003
+    g = 10.0 ** (torch.rand(n, device="cuda", generator=gen(10)) * 40 - 25) * torch.randn(n, device="cuda", generator=gen(11)).sign()
+    m = g * torch.rand(n, device="cuda", generator=gen(12))
+    v = (g * g) * torch.rand(n, device="cuda", generator=gen(13))
+    p = torch.zeros(n, device="cuda")
+    w = None if work is None else [torch.zeros(n, dtype=TYPES[work], device="cuda")]
+    old = [host(x) for x in (p, g, m, v)]
+    for step in (1, 1000, 2_000_000):
+        pp, mm, vv = p.clone(), m.clone(), v.clone()
+        sp.adam_step_tensors(sp.adam_list([pp], [g], [mm], [vv], lr=2.0 ** -7, params_work=w), 0.9, 0.999, 1e-15, step=step)
+        h = dict(step=step, lr=2.0 ** -7, b1=0.9, b2=0.999, eps=1e-15)
+        for name, got, want, b in zip("pmv", (pp, mm, vv), tl.adamw_step(*old, **h), tt.adam_bounds(*old, **h)):
+            tt.within(host(got), want, b, "step %d %s" % (step, name))
+        if w:
+            assert torch.equal(w[0], pp.to(TYPES[work]))
+
+
+def test_two_graphs_with_the_default_workspace(sp):
+    """Each capture gets a workspace of its own; replayed in turn and on two streams at once they do not meet."""
+    lens = [400_000, 3, 70_001]
+    sides = []
+    for k in range(2):
+        views, flat, before = packed(lens, "f32", 300 + k)
+        ctl, graph, stream = sp.grad_control(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        lst = sp.grad_list(views)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            sp.grad_norm(lst, ctl, max_norm=1.0)
+        sides.append((views, ctl, graph, stream))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for _, _, graph, stream in sides:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for views, ctl, _, _ in sides:
+        want, coef, _ = tl.grad_norm([host(v) for v in views], max_norm=1.0)
+        tt.within(host(ctl.norm), want, tt.scalar_bound(want), "norm")
+        tt.within(host(ctl.coef), coef, tt.scalar_bound(coef), "coef")
+        assert int(ctl.step) == 10
 
 
 def test_shared_gradient(sp):
