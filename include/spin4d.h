@@ -290,8 +290,10 @@ int spin4d_adam_step(float* params, void* params_work, float* grad, float* m, fl
  * SPIN4D_MAX_LIST_TENSORS tensors; a tensor has n >= 0 contiguous values
  * (n == 0: its pointers are not looked at), at most 2^40, aligned to its
  * type's size; a list spans at most about 2^42 values.  Any alignment beyond
- * that is handled; arrays of one tensor that start at different offsets from
- * a 32-byte (fp16 and bf16: 16-byte) boundary take a slower path.
+ * that is handled; where the arrays that a call writes of one tensor start at
+ * different offsets (in values) from a 32-byte boundary (fp16 and bf16:
+ * 16-byte), it takes a slower path.  A gradient that is only read may start
+ * anywhere.
  */
 #define SPIN4D_MAX_LIST_TENSORS 65536
 

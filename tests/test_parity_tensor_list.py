@@ -270,6 +270,27 @@ def test_adam_step_with_arrays_at_different_offsets(sp):
     assert int(flag) == 0
 
 
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_adam_step_with_gradients_from_a_packed_bucket(sp, dtype, zero):
+    """Parameters and state of their own, gradients at every offset of one buffer: read, and cleared, in place."""
+    lens = EDGES
+    own = [_adam_state([n], "f32", 500 + 10 * k, gap=8, work="f16") for k, n in enumerate(lens)]
+    p, m, v, w = ([x[0][j][0] for x in own] for j in (0, 2, 3, 4))
+    for gap in (1, 2, 3):
+        g, gf, g0 = packed(lens, dtype, 700 + gap, gap=gap)
+        old = [[host(x) for x in a] for a in (p, g, m, v)]
+        sp.adam_step_tensors(sp.adam_list(p, g, m, v, lr=1e-2, params_work=w), 0.9, 0.99, 1e-8, step=2, zero_grad=zero)
+        for k, n in enumerate(lens):
+            args = [a[k] for a in old]
+            h = dict(step=2, lr=1e-2, b1=0.9, b2=0.99, eps=1e-8)
+            for name, got, want, b in zip("pmv", (p[k], m[k], v[k]), tl.adamw_step(*args, **h), tt.adam_bounds(*args, **h)):
+                tt.within(host(got), want, b, "%s of %d" % (name, n))
+            assert torch.equal(w[k], p[k].half())
+        gaps_unchanged(gf, g0, lens, gap)
+        assert all(not x.any() for x in g) if zero else torch.equal(gf, g0)
+
+
 @pytest.mark.parametrize("count", [1, 17, 512, 513, 1300])
 def test_adam_step_of_many_tensors(sp, count):
     lens = [int(x) for x in np.random.default_rng(count).integers(0, 300, count)]
