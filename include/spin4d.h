@@ -348,9 +348,9 @@ int spin4d_grad_norm(const spin4d_grad_tensor* tensors, int count, int norm_type
 /*
  * out = control->coef * grad for every tensor, in fp32 and rounded to the
  * output's type; coef == 0 writes zeros whatever the gradient holds, so that a
- * gradient with a NaN is dropped whole.  In place, coef == 1 writes nothing.  SPIN4D_ERR_INVALID when an output
- * overlaps another array of the list (its own gradient in the same type, that
- * is in place, excepted).
+ * gradient with a NaN is dropped whole.  In place, coef == 1 writes nothing.
+ * SPIN4D_ERR_INVALID when an output overlaps another array of the list (its
+ * own gradient in the same type, that is in place, excepted).
  */
 int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, const spin4d_grad_control* control,
                       spin4d_stream_t stream);
