@@ -148,18 +148,11 @@ __device__ __forceinline__ void load_raw(const void* a, Raw<2>& r) {
                  : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
                  : "l"(a) : "memory");
 }
-template <Hint H>
 __device__ __forceinline__ void store_raw(void* a, const Raw<4>& r) {
-  if (H == kStream)
-    asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(a),
-                 "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
-                 : "memory");
-  else
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(a), "r"(r.w[0]), "r"(r.w[1]),
-                 "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
-                 : "memory");
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(a), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+               "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+               : "memory");
 }
-template <Hint H>
 __device__ __forceinline__ void store_raw(void* a, const Raw<2>& r) {
   asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(a), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3])
                : "memory");
@@ -242,36 +235,33 @@ __device__ __forceinline__ void fetch(const void* a, const Places& q, Raw<2>& r,
     for (int i = 0; i < 4; ++i) r.w[i] = h[2 * i] | h[2 * i + 1] << 16;
   }
 }
-template <Hint H>
 __device__ __forceinline__ void put(void* a, const Places& q, const Raw<4>& r) {
   if (q.whole) {
-    store_raw<H>(static_cast<float*>(a) + q.first, r);
+    store_raw(static_cast<float*>(a) + q.first, r);
   } else {
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
       if (q.has(i)) static_cast<uint32_t*>(a)[q.place(i)] = r.w[i];
   }
 }
-template <Hint H>
 __device__ __forceinline__ void put(void* a, const Places& q, const Raw<2>& r) {
   if (q.whole) {
-    store_raw<H>(static_cast<uint16_t*>(a) + q.first, r);
+    store_raw(static_cast<uint16_t*>(a) + q.first, r);
   } else {
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
       if (q.has(i)) static_cast<uint16_t*>(a)[q.place(i)] = (uint16_t)(r.w[i / 2] >> 16 * (i & 1));
   }
 }
-template <Hint H>
 __device__ __forceinline__ void put(void* a, int dt, const Places& q, const float x[kVec]) {
   if (dt == SPIN4D_F32) {
     Raw<4> r;
     pack(x, false, r);
-    put<H>(a, q, r);
+    put(a, q, r);
   } else {
     Raw<2> r;
     pack(x, dt == SPIN4D_BF16, r);
-    put<H>(a, q, r);
+    put(a, q, r);
   }
 }
 
@@ -566,7 +556,7 @@ __device__ __forceinline__ void clip_tiles(const void* a, void* o, const Meta me
 #pragma unroll
         for (int i = 0; i < kVec; ++i) x[i] = coef == 0.0f ? 0.0f : coef * x[i];   // zeros whatever the gradient holds
         // kept: the optimiser reads it next (norm, clip and Adam of 4M values 28.9 us, streamed 30.0)
-        put<kKeep>(o, meta.out_dtype(), Places(stop - 1 - u, shift, n), x);
+        put(o, meta.out_dtype(), Places(stop - 1 - u, shift, n), x);
       }
     stop -= min((uint32_t)kAhead, stop - t);
   }
@@ -597,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Adam with decoupled weight decay, formula in the header.  Four streams in,
 // three and the working copy out: bound by HBM, 134M parameters with fp16
-// copies (30 bytes each) in 594 us, 6.8 TB/s; 16.8M in 74.  80 registers for 128
+// copies (30 bytes each) in 595 us, 6.8 TB/s; 16.8M in 74.  72 registers for 128
 // bytes of loads a thread, three blocks a SM; the first loads are on their way
 // before the control block is read, and in L2 before the norm has ended.
 // ---------------------------------------------------------------------------
@@ -683,18 +673,18 @@ __global__ void __launch_bounds__(kThreads, 3) adam_list_kernel(const __grid_con
 #pragma unroll
           for (int i = 0; i < kVec; ++i) bad |= !isfinite(p[i]) && (q.whole || q.has(i));
         }
-        put<kKeep>(e.p, SPIN4D_F32, q, p);
-        put<kKeep>(e.m, SPIN4D_F32, q, m);
-        put<kKeep>(e.v, SPIN4D_F32, q, v);
+        put(e.p, SPIN4D_F32, q, p);
+        put(e.m, SPIN4D_F32, q, m);
+        put(e.v, SPIN4D_F32, q, v);
         if (e.work) {
           Raw<2> w;
           pack(p, e.meta.out_dtype() == SPIN4D_BF16, w);
-          put<kKeep>(e.work, q, w);
+          put(e.work, q, w);
         }
       }
       if (a.zero_grad) {
         const float zero[kVec] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        put<kKeep>(e.g, e.meta.dtype(), q, zero);
+        put(e.g, e.meta.dtype(), q, zero);
       }
     }
     end = stop;
