@@ -6,6 +6,7 @@ the library is missing the import fails loudly; there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import itertools
 import os
@@ -213,6 +214,18 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream, device):
+    """The context in which a call on ``stream`` (None: the current one) allocates.  A block of the caching allocator is
+    ordered along the stream it was taken on; of the current stream's, work that is pending there may still be using it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        # 0 and 1: the handles of the legacy default stream
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
+    return torch.cuda.stream(stream)
 
 
 _DT = {"f32": F32, "f16": F16, torch.float32: F32, torch.float16: F16}
@@ -536,7 +549,7 @@ def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_
     ``control.step`` goes up by one where the norm is finite,
     ``control.skipped`` where it is not.  grads: a GradList or tensors.  norms:
     a float32 tensor that gets each tensor's own norm.  The workspace (uint8
-    device tensor) is allocated when not given."""
+    device tensor) is allocated on the call's stream when not given."""
     if type(grads) is not GradList:
         grads = GradList(grads)
     kind = _NORMS.get(norm_type)
@@ -551,10 +564,8 @@ def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_
             raise ValueError("norms: one contiguous float32 value for each tensor, on the list's device")
         norms_at = norms.data_ptr() or None
     if workspace is None:
-        workspace = torch.empty(grad_norm_workspace(grads.count), dtype=torch.uint8, device=control.device)
-        if stream is not None:      # the allocator must not hand it on before that stream is done with it
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(_stream(stream), control.device))
+        with _on(stream, control.device):
+            workspace = torch.empty(grad_norm_workspace(grads.count), dtype=torch.uint8, device=control.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous, on the list's device")
     _list_call("spin4d_grad_norm", index, stream,
