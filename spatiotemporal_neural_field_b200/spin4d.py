@@ -276,13 +276,15 @@ def hex_from_spec(spec) -> HexDesc:
 
 
 # ---------------------------------------------------------------------------
-# Calls
+# Calls.  With ``stream`` the kernels run there, and what a call allocates by
+# itself (outputs, workspaces, zeroed gradients) belongs to that stream.
 # ---------------------------------------------------------------------------
 def encode_fwd(g: GridDesc, pos: torch.Tensor, tables: torch.Tensor, z: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
     N = pos.shape[0]
     if z is None:
-        z = torch.empty((N, g.L * g.F), dtype=torch.float32, device=pos.device)
+        with _on(stream, pos.device):
+            z = torch.empty((N, g.L * g.F), dtype=torch.float32, device=pos.device)
     _check("spin4d_encode_fwd", lib.spin4d_encode_fwd(ctypes.byref(g), _ptr(pos), N, _ptr(tables), _ptr(z),
                                                       _stream(stream)))
     return z
@@ -302,7 +304,8 @@ def decode_fwd(g: GridDesc, m: MlpDesc, pos: torch.Tensor, tables: torch.Tensor,
                stream=None) -> Dict[str, torch.Tensor]:
     N = pos.shape[0]
     if out is None:
-        out = alloc_outputs(N, pos.device)
+        with _on(stream, pos.device):
+            out = alloc_outputs(N, pos.device)
     o = Outputs(*(_ptr(out.get(k)) for k in ("scale", "rot", "rgb", "opacity", "cov", "latent")))
     _check("spin4d_decode_fwd", lib.spin4d_decode_fwd(ctypes.byref(g), ctypes.byref(m), _ptr(pos), N, _ptr(tables),
                                                       _ptr(weights), _ptr(gate_cr), o, _stream(stream)))
@@ -325,7 +328,8 @@ def decode_bwd(g: GridDesc, m: MlpDesc, pos, tables, weights, grads: Dict[str, t
     N = pos.shape[0]
     need = decode_bwd_workspace(g, m, N)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=pos.device)
+        with _on(stream, pos.device):
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=pos.device)
     go = OutputGrads(*(_ptr(grads.get(k)) for k in ("scale", "rot", "rgb", "opacity", "cov")))
     common = (ctypes.byref(g), ctypes.byref(m), _ptr(pos), N, _ptr(tables), _ptr(weights), _ptr(gate_cr),
               _ptr(latent), ctypes.byref(go), _ptr(grad_tables), _ptr(grad_weights))
@@ -358,7 +362,8 @@ def decode_bwd_noalloc(g: GridDesc, m: MlpDesc, pos, tables, weights, grads: Dic
 def cov_assemble(scale: torch.Tensor, rot: torch.Tensor, cov: Optional[torch.Tensor] = None, stream=None):
     N = scale.shape[0]
     if cov is None:
-        cov = torch.empty((N, 6), dtype=torch.float32, device=scale.device)
+        with _on(stream, scale.device):
+            cov = torch.empty((N, 6), dtype=torch.float32, device=scale.device)
     _check("spin4d_cov_assemble", lib.spin4d_cov_assemble(_ptr(scale), _ptr(rot), N, _ptr(cov), _stream(stream)))
     return cov
 
@@ -630,14 +635,16 @@ def heads_fwd(g: GridDesc, h: HeadsDesc, pos, tables, weights, out=None, latent:
     N = pos.shape[0]
     if isinstance(workspace, str):
         need = lib.spin4d_heads_fwd_workspace(ctypes.byref(g), ctypes.byref(h), N)
-        workspace = torch.empty(need, dtype=torch.uint8, device=pos.device) if need else None
+        with _on(stream, pos.device):
+            workspace = torch.empty(need, dtype=torch.uint8, device=pos.device) if need else None
     widths = {"scale": 3, "rot": 4, "sh": h.sh_dim, "opacity": 1, "cov": 6}
     if out is None:
-        out = {k: torch.empty((N, w), dtype=torch.float32, device=pos.device) for k, w in widths.items()}
         if latent:
-            out["latent"] = torch.empty((N, h.in_dim), dtype=torch.float32, device=pos.device)
+            widths["latent"] = h.in_dim
         if raw:
-            out["raw"] = torch.empty((N, 8), dtype=torch.float32, device=pos.device)
+            widths["raw"] = 8
+        with _on(stream, pos.device):
+            out = {k: torch.empty((N, w), dtype=torch.float32, device=pos.device) for k, w in widths.items()}
     o = HeadsOutputs(*(_ptr(out[k]) for k in HEADS_KEYS), _ptr(out.get("latent")), _ptr(out.get("raw")))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("spin4d_heads_fwd", lib.spin4d_heads_fwd(ctypes.byref(g), ctypes.byref(h), _ptr(pos), N, _ptr(tables),
@@ -654,7 +661,8 @@ def heads_bwd(g: GridDesc, h: HeadsDesc, pos, tables, weights, grads, grad_table
     N = pos.shape[0]
     if workspace is None:
         need = int(lib.spin4d_heads_bwd_workspace(ctypes.byref(g), ctypes.byref(h), N))
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=pos.device)
+        with _on(stream, pos.device):
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=pos.device)
     go = HeadsOutputGrads(*(_ptr(grads.get(k)) for k in HEADS_KEYS))
     _check("spin4d_heads_bwd", lib.spin4d_heads_bwd(ctypes.byref(g), ctypes.byref(h), _ptr(pos), N, _ptr(tables),
                                                     _ptr(weights), _ptr(latent), _ptr(raw), ctypes.byref(go),
@@ -680,7 +688,8 @@ def hexplane_fwd(h: HexDesc, inp: Dict[str, torch.Tensor], planes, weights, out=
     window gates the deformation (spin4d_hexplane_fwd_gated)."""
     N = inp["mu"].shape[0]
     if out is None:
-        out = {k: torch.empty((N, w), dtype=torch.float32, device=planes.device) for k, w in HEX_KEYS}
+        with _on(stream, planes.device):
+            out = {k: torch.empty((N, w), dtype=torch.float32, device=planes.device) for k, w in HEX_KEYS}
     o = HexOutputs(*(_ptr(out[k]) for k, _ in HEX_KEYS), _ptr(out.get("latent")), _ptr(out.get("hidden")))
     common = (ctypes.byref(h), _ptr(inp["mu"]), _ptr(inp["frame"]), N, _ptr(planes), _ptr(weights),
               _ptr(inp["q_can"]), _ptr(inp["logs_can"]), _ptr(inp["sh_can"]))
@@ -706,7 +715,8 @@ def hexplane_bwd(h: HexDesc, inp, planes, weights, grads, grad_planes, grad_weig
     spin4d_hexplane_bwd_saved."""
     N = inp["mu"].shape[0]
     if workspace is None:
-        workspace = torch.empty(max(hexplane_bwd_workspace(h, N), 1), dtype=torch.uint8, device=planes.device)
+        with _on(stream, planes.device):
+            workspace = torch.empty(max(hexplane_bwd_workspace(h, N), 1), dtype=torch.uint8, device=planes.device)
     go = HexOutputGrads(*(_ptr(grads.get(k)) for k, _ in HEX_KEYS))
     common = (ctypes.byref(h), _ptr(inp["mu"]), _ptr(inp["frame"]), N, _ptr(planes), _ptr(weights),
               _ptr(inp["q_can"]), _ptr(inp["logs_can"]), _ptr(inp["sh_can"]), _ptr(latent))
@@ -726,8 +736,9 @@ def hexplane_bwd(h: HexDesc, inp, planes, weights, grads, grad_planes, grad_weig
 
 def debug_corners(g: GridDesc, pos: torch.Tensor, stream=None):
     N = pos.shape[0]
-    idx = torch.empty((N, g.L, 16), dtype=torch.int32, device=pos.device)
-    frac = torch.empty((N, g.L, 4), dtype=torch.float32, device=pos.device)
+    with _on(stream, pos.device):
+        idx = torch.empty((N, g.L, 16), dtype=torch.int32, device=pos.device)
+        frac = torch.empty((N, g.L, 4), dtype=torch.float32, device=pos.device)
     _check("spin4d_debug_corners", lib.spin4d_debug_corners(ctypes.byref(g), _ptr(pos), N, _ptr(idx), _ptr(frac),
                                                             _stream(stream)))
     return idx, frac
@@ -741,11 +752,12 @@ def check_device_errors(clear: bool = True) -> None:
 def morton_order(g: GridDesc, pos: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None):
     """(sorted 30-bit Z-order keys, permutation), both N int32 holding uint32 values."""
     N = pos.shape[0]
-    keys = torch.empty(N, dtype=torch.int32, device=pos.device)
-    perm = torch.empty(N, dtype=torch.int32, device=pos.device)
     need = int(lib.spin4d_morton_order_workspace(N))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=pos.device)
+    with _on(stream, pos.device):
+        keys = torch.empty(N, dtype=torch.int32, device=pos.device)
+        perm = torch.empty(N, dtype=torch.int32, device=pos.device)
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=pos.device)
     _check("spin4d_morton_order", lib.spin4d_morton_order(ctypes.byref(g), _ptr(pos), N, _ptr(keys), _ptr(perm),
                                                           _ptr(workspace), workspace.numel(), _stream(stream)))
     return keys, perm
@@ -755,7 +767,8 @@ def permute_rows(src: torch.Tensor, perm: torch.Tensor, out: Optional[torch.Tens
     """out[i] = src[perm[i]] along the first dimension (contiguous tensors)."""
     N = perm.shape[0]
     if out is None:
-        out = torch.empty((N,) + tuple(src.shape[1:]), dtype=src.dtype, device=src.device)
+        with _on(stream, src.device):
+            out = torch.empty((N,) + tuple(src.shape[1:]), dtype=src.dtype, device=src.device)
     row_bytes = src[0].numel() * src.element_size() if src.dim() > 1 else src.element_size()
     _check("spin4d_permute_rows", lib.spin4d_permute_rows(_ptr(src), src.shape[0], _ptr(out), _ptr(perm), N,
                                                           row_bytes, _stream(stream)))
@@ -829,10 +842,11 @@ def render_fwd(cam: Camera, desc: RenderDesc, means, cov, opacity, colours, imag
     ``state.pairs_needed() <= state.max_pairs`` (or use ``render``)."""
     N = means.shape[0]
     dev = means.device
-    if state is None:
-        state = RenderState(N, cam.width, cam.height, default_max_pairs(N, cam.width, cam.height), dev)
-    if image is None:
-        image = torch.empty((3, cam.height, cam.width), dtype=torch.float32, device=dev)
+    with _on(stream, dev):
+        if state is None:
+            state = RenderState(N, cam.width, cam.height, default_max_pairs(N, cam.width, cam.height), dev)
+        if image is None:
+            image = torch.empty((3, cam.height, cam.width), dtype=torch.float32, device=dev)
     _check("spin4d_render_fwd", lib.spin4d_render_fwd(ctypes.byref(cam), ctypes.byref(desc), N, _ptr(means),
                                                       _ptr(cov), _ptr(opacity), _ptr(colours), _ptr(image),
                                                       _ptr(final_T), _ptr(state.buf), state.buf.numel(),
@@ -860,10 +874,11 @@ def render_bwd(cam: Camera, desc: RenderDesc, means, cov, opacity, colours, grad
     N = means.shape[0]
     dev = means.device
     z = lambda shape: torch.zeros(shape, dtype=torch.float32, device=dev)   # noqa: E731
-    grad_means = z((N, 3)) if grad_means is None else grad_means
-    grad_cov = z((N, 6)) if grad_cov is None else grad_cov
-    grad_opacity = z((N,)) if grad_opacity is None else grad_opacity
-    grad_colours = z(tuple(colours.shape)) if grad_colours is None else grad_colours
+    with _on(stream, dev):
+        grad_means = z((N, 3)) if grad_means is None else grad_means
+        grad_cov = z((N, 6)) if grad_cov is None else grad_cov
+        grad_opacity = z((N,)) if grad_opacity is None else grad_opacity
+        grad_colours = z(tuple(colours.shape)) if grad_colours is None else grad_colours
     _check("spin4d_render_bwd", lib.spin4d_render_bwd(ctypes.byref(cam), ctypes.byref(desc), N, _ptr(means),
                                                       _ptr(cov), _ptr(opacity), _ptr(colours), _ptr(grad_image),
                                                       _ptr(state.buf), state.buf.numel(), state.max_pairs,

@@ -8,6 +8,8 @@ import contextlib
 import pytest
 import torch
 
+from tests import tol
+
 
 class Side:
     """A stream by its handle, as torch.cuda.Stream has it."""
@@ -97,3 +99,65 @@ def test_a_freed_block_with_work_pending_is_not_the_workspace(sp):
         torch.cuda.synchronize()
         assert int(total) == 3 * need
         assert int(ctl.step) == 2 + i and abs(float(ctl.norm) - (70_001 / 4) ** 0.5) <= 2.0 ** -24 * 200
+
+
+def calls(sp):
+    """Every other call that allocates a workspace or outputs, by name: (call of a stream, allocations)."""
+    t, i = torch.Tensor, lambda *shape: torch.Tensor(*shape).int()   # noqa: E731
+    g, m = sp.GridDesc(L=2, F=2), sp.MlpDesc(in_dim=4, hidden=8, n_hidden=1)
+    h, hx = sp.HeadsDesc(in_dim=4, hidden=8, sh_dim=48), sp.HexDesc()
+    cam, desc = sp.camera([[1, 0, 0, 0], [0, 1, 0, 0], [0, 0, 1, 0]], 1, 1, 0, 0, 32, 16), sp.render_desc()
+    pos, w = t(5, 4), t(9)
+    hex_in = dict(mu=t(5, 3), frame=i(5), q_can=t(5, 4), logs_can=t(5, 3), sh_can=t(5, 48))
+    scene = (t(5, 3), t(5, 6), t(5), t(5, 48))
+    state = object.__new__(sp.RenderState)
+    state.buf, state.max_pairs = torch.zeros(64, dtype=torch.uint8), 1 << 20
+    return {
+        "encode_fwd": (lambda s: sp.encode_fwd(g, pos, w, stream=s), 1),
+        "decode_fwd": (lambda s: sp.decode_fwd(g, m, pos, w, w, stream=s), 5),
+        "decode_bwd": (lambda s: sp.decode_bwd(g, m, pos, w, w, {}, w, w, stream=s), 1),
+        "cov_assemble": (lambda s: sp.cov_assemble(t(5, 3), t(5, 4), stream=s), 1),
+        "heads_fwd": (lambda s: sp.heads_fwd(g, h, pos, w, w, latent=True, raw=True, stream=s), 8),
+        "heads_bwd": (lambda s: sp.heads_bwd(g, h, pos, w, w, {}, w, w, stream=s), 1),
+        "hexplane_fwd": (lambda s: sp.hexplane_fwd(hx, hex_in, w, w, stream=s), 5),
+        "hexplane_bwd": (lambda s: sp.hexplane_bwd(hx, hex_in, w, w, {}, w, w, stream=s), 1),
+        "debug_corners": (lambda s: sp.debug_corners(g, pos, stream=s), 2),
+        "morton_order": (lambda s: sp.morton_order(g, pos, stream=s), 3),
+        "permute_rows": (lambda s: sp.permute_rows(w, i(5), stream=s), 1),
+        "render_fwd": (lambda s: sp.render_fwd(cam, desc, *scene, stream=s), 2),
+        "render_bwd": (lambda s: sp.render_bwd(cam, desc, *scene, t(3, 16, 32), state, stream=s), 4),
+    }
+
+
+@pytest.mark.parametrize("name", ["encode_fwd", "decode_fwd", "decode_bwd", "cov_assemble", "heads_fwd", "heads_bwd",
+                                  "hexplane_fwd", "hexplane_bwd", "debug_corners", "morton_order", "permute_rows",
+                                  "render_fwd", "render_bwd"])
+def test_calls_allocate_on_the_stream_they_run_on(sp, seen, monkeypatch, name):
+    call, count = calls(sp)[name]
+    side = Side()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: Side())
+    for stream, want in ((None, None), (side, side)):
+        del seen[:]
+        call(stream)
+        assert [w for _, w in seen] == [want] * count
+
+
+@pytest.mark.gpu
+def test_render_gradients_are_zeroed_on_the_stream_of_the_call(sp):
+    """With work pending on the current stream the zeros still come before the kernel that adds to them."""
+    cam, desc = sp.camera([[1, 0, 0, 0], [0, 1, 0, 0], [0, 0, 1, 3]], 40, 40, 30, 22, 60, 44), sp.render_desc()
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *shape: torch.rand(shape, device="cuda", generator=gen)   # noqa: E731
+    cov = torch.tensor([1e-2, 0, 0, 1e-2, 0, 1e-2], device="cuda").repeat(200, 1)
+    scene = (r(200, 3) - 0.5, cov, r(200) * 0.5 + 0.2, r(200, 48) - 0.5)
+    image_grad, side = r(3, 44, 60), torch.cuda.Stream()
+    _, state = sp.render(cam, desc, *scene)
+    want = sp.render_bwd(cam, desc, *scene, image_grad, state)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(4_000_000)
+    got = sp.render_bwd(cam, desc, *scene, image_grad, state, stream=side)
+    torch.cuda.synchronize()
+    for k in want:
+        # the same sums by atomics in another order: the bound that other tests have between two such runs
+        assert bool(want[k].any())
+        tol.normwise(got[k].cpu().numpy(), want[k].cpu().numpy(), 1e-4, k)
