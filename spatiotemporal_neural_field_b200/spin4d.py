@@ -825,7 +825,8 @@ class RenderState:
         self.buf = torch.empty(need, dtype=torch.uint8, device=device)
 
     def pairs_needed(self) -> int:
-        """(Gaussian, tile) pairs the last forward needed; synchronises."""
+        """(Gaussian, tile) pairs the last forward needed; synchronises with
+        the current stream, which has to be the forward's or behind it."""
         return int(self.buf[:8].view(torch.int64).item())
 
     def pairs_kept(self) -> int:
@@ -859,9 +860,11 @@ def render(cam: Camera, desc: RenderDesc, means, cov, opacity, colours, final_T=
     """Forward render that grows the pair capacity until the frame fits
     (one host synchronisation per attempt)."""
     image, state = render_fwd(cam, desc, means, cov, opacity, colours, final_T=final_T, state=state, stream=stream)
-    need = state.pairs_needed()
+    with _on(stream, means.device):     # the read waits for the stream that it is made on
+        need = state.pairs_needed()
     if need > state.max_pairs:
-        state = RenderState(means.shape[0], cam.width, cam.height, need, means.device)
+        with _on(stream, means.device):
+            state = RenderState(means.shape[0], cam.width, cam.height, need, means.device)
         image, state = render_fwd(cam, desc, means, cov, opacity, colours, image=image, final_T=final_T,
                                   state=state, stream=stream)
     return image, state

@@ -161,3 +161,39 @@ def test_render_gradients_are_zeroed_on_the_stream_of_the_call(sp):
         # the same sums by atomics in another order: the bound that other tests have between two such runs
         assert bool(want[k].any())
         tol.normwise(got[k].cpu().numpy(), want[k].cpu().numpy(), 1e-4, k)
+
+
+def test_render_reads_the_pair_count_on_the_stream_of_the_call(sp, seen, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: Side())
+    cam, desc = sp.camera([[1, 0, 0, 0], [0, 1, 0, 0], [0, 0, 1, 0]], 1, 1, 0, 0, 32, 16), sp.render_desc()
+    t, side = torch.Tensor, Side()
+    for stream, want in ((None, None), (side, side)):
+        state = object.__new__(sp.RenderState)
+        state.buf, state.max_pairs = torch.zeros(64, dtype=torch.uint8), 1 << 20
+        del seen[:]
+        sp.render(cam, desc, t(5, 3), t(5, 6), t(5), t(5, 48), state=state, stream=stream)
+        assert [w for what, w in seen if what == "item"] == [want]
+
+
+@pytest.mark.gpu
+def test_render_on_a_stream_grows_its_state_and_gives_the_image(sp):
+    """A state that is too small, on a stream with work pending: the pair count is read after the forward."""
+    cam, desc = sp.camera([[1, 0, 0, 0], [0, 1, 0, 0], [0, 0, 1, 3]], 400, 400, 300, 220, 600, 440), sp.render_desc()
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *shape: torch.rand(shape, device="cuda", generator=gen)   # noqa: E731
+    cov = torch.tensor([1e-1, 0, 0, 1e-1, 0, 1e-1], device="cuda").repeat(400, 1)
+    scene = (r(400, 3) - 0.5, cov, r(400) * 0.5 + 0.2, r(400, 48) - 0.5)
+    want, full = sp.render(cam, desc, *scene)
+    few = (600 // 16 + 1) * (440 // 16 + 1)
+    assert full.pairs_needed() > few
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    state = sp.RenderState(400, 600, 440, few, "cuda")
+    state.buf.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(4_000_000)
+    got, grown = sp.render(cam, desc, *scene, state=state, stream=side)
+    torch.cuda.synchronize()
+    assert grown is not state and grown.max_pairs == full.pairs_needed()
+    assert torch.equal(got, want)
