@@ -328,7 +328,7 @@ size_t spin4d_grad_norm_workspace(int count);
 /*
  * norm = the norm of grad_scale * g over all tensors of the list, and
  *   coef = grad_scale * min(1, max_norm / (norm + 1e-6)).
- * grad_scale (> 0, finite) undoes a loss scale or averages a sum over ranks;
+ * grad_scale (in fp32 > 0 and finite) undoes a loss scale or averages a sum over ranks;
  * max_norm >= 0, INFINITY to measure only.  Where the norm is not a finite
  * fp32 number (a NaN or infinity in any gradient), coef is 0, `step` stays and
  * `skipped` counts it.  norms (optional, `count` fp32 values): each tensor's

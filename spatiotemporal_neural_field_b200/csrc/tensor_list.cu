@@ -905,7 +905,9 @@ extern "C" int spin4d_grad_norm(const spin4d_grad_tensor* tensors, int count, in
                                 size_t ws_bytes, spin4d_stream_t stream) {
   if (count < 0 || count > kMaxTensors || (count > 0 && !tensors)) return SPIN4D_ERR_INVALID;
   if (norm_type != kL1 && norm_type != kL2 && norm_type != kMax) return SPIN4D_ERR_INVALID;
-  if (!(grad_scale > 0.0) || !isfinite(grad_scale) || !(max_norm >= 0.0)) return SPIN4D_ERR_INVALID;
+  // as the coefficient holds it: infinite it would make NaN of a zero gradient, 0 is the one that drops a gradient
+  const float scale32 = (float)grad_scale;
+  if (!(scale32 > 0.0f) || !isfinite(scale32) || !(max_norm >= 0.0)) return SPIN4D_ERR_INVALID;
   if (!control || !aligned(control, 16) || (norms && !aligned(norms, 4))) return SPIN4D_ERR_INVALID;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < spin4d_grad_norm_workspace(count)) return SPIN4D_ERR_INVALID;
   int64_t tiles = 0;
