@@ -378,7 +378,7 @@ typedef struct spin4d_adam_tensor {
  *   p -= lr * (m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps) + lr * weight_decay * p
  * t = step when step > 0, else control->step (which spin4d_grad_norm has
  * advanced).  The square root is within 2^-23 of itself and the quotient within
- * 2 ulp.  Where control->norm is not finite (or t < 1) params, params_work, m
+ * 2 ulp; for that eps is 0 or, in fp32, from 2^-126 to 2^125.  Where control->norm is not finite (or t < 1) params, params_work, m
  * and v stay as they are.  zero_grad != 0 clears the gradients in either
  * case.  nonfinite_flag as in spin4d_adam_step.  SPIN4D_ERR_INVALID when an
  * array that is written overlaps another one of the list; gradients that are

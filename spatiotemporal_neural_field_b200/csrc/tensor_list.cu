@@ -966,8 +966,10 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
   if (count < 0 || count > kMaxTensors || (count > 0 && !tensors)) return SPIN4D_ERR_INVALID;
   if (step < 0 || (step == 0 && !control)) return SPIN4D_ERR_INVALID;
   // as the kernel holds them: a rate that rounds to 1 would never forget
-  if (!(b1 >= 0.0 && (float)b1 < 1.0f && b2 >= 0.0 && (float)b2 < 1.0f && eps >= 0.0 && isfinite((float)eps)))
-    return SPIN4D_ERR_INVALID;
+  if (!(b1 >= 0.0 && (float)b1 < 1.0f && b2 >= 0.0 && (float)b2 < 1.0f && eps >= 0.0)) return SPIN4D_ERR_INVALID;
+  // the quotient holds to its bound for denominators from 2^-126 to 2^126, of which the root takes up to 2^64
+  const float eps32 = (float)eps;
+  if (eps32 != 0.0f && !(eps32 >= 0x1p-126f && eps32 <= 0x1p125f)) return SPIN4D_ERR_INVALID;
   if ((control && !aligned(control, 16)) || (nonfinite_flag && !aligned(nonfinite_flag, 4))) return SPIN4D_ERR_INVALID;
   int64_t tiles = 0;
   for (int k = 0; k < count; ++k) {
@@ -999,7 +1001,7 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
   a.b2 = (float)b2;
   a.omb1 = (float)(1.0 - b1);
   a.omb2 = (float)(1.0 - b2);
-  a.eps = (float)eps;
+  a.eps = eps32;
   a.log_b1 = log(b1);
   a.log_b2 = log(b2);
   a.step = step;

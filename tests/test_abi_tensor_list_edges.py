@@ -58,3 +58,17 @@ def test_grad_norm_takes_scales_that_round_into_fp32(sp):
               2.0 ** -149, 1.001 * 2.0 ** -150, 1.0]
     call = "sp.lib.spin4d_grad_norm((sp.GradTensor * 1)(sp.GradTensor(F, None, 9, 0, 0)), 1, 2, %r, 1.0, F, None, F, 1 << 20, None)"
     assert statuses("spin4d_grad_norm", [call % x for x in scales]) == [sp.ERR_INJECTED] * len(scales)
+
+
+ADAM = ("sp.lib.spin4d_adam_step_tensors((sp.AdamTensor * 1)(sp.AdamTensor(F, None, F + S, F + 2 * S, F + 3 * S, 9, 1e-3,"
+        " 0.0, 0, 0)), 1, 1, 0.9, 0.99, %r, 0, None, None, None)")
+
+
+def test_adam_refuses_eps_outside_the_range_of_its_quotient(sp):
+    """The quotient is within 2 ulp for denominators from 2^-126 to 2^126 (and 0, where it is infinite or NaN as it should
+    be); the root reaches 2^64."""
+    taken = [0.0, 2.0 ** -126, 1e-30, 1e-15, 1e-8, 1.0, 2.0 ** 125]
+    refused = [2.0 ** -149, 1e-40, 2.0 ** -127, 2.0 ** 125 * (1 + 2.0 ** -23), 2.0 ** 126, 1e38, FMAX]
+    assert statuses("spin4d_adam_step_tensors", [ADAM % x for x in taken]) == [sp.ERR_INJECTED] * len(taken)
+    assert statuses("spin4d_adam_step_tensors", [ADAM % x for x in refused]) == [sp.ERR_INVALID] * len(refused)
+    assert statuses("spin4d_adam_step_tensors", [ADAM % 1e-46]) == [sp.ERR_INJECTED]      # 0 in fp32
