@@ -939,7 +939,7 @@ extern "C" int spin4d_clip_grads(const spin4d_grad_tensor* tensors, int count, c
   int64_t tiles = 0;
   for (int k = 0; k < count; ++k) {
     const spin4d_grad_tensor& t = tensors[k];
-    if (t.n < 0 || t.n > kMaxValues || !dtype_ok(t.grad_dtype) || (t.out && !dtype_ok(t.out_dtype)))
+    if (t.n < 0 || t.n > kMaxValues || !dtype_ok(t.grad_dtype) || (t.n && t.out && !dtype_ok(t.out_dtype)))
       return SPIN4D_ERR_INVALID;
     if (!array_ok(t.grad, t.n, dtype_bytes(t.grad_dtype))) return SPIN4D_ERR_INVALID;
     if (t.out && !array_ok(t.out, t.n, dtype_bytes(t.out_dtype))) return SPIN4D_ERR_INVALID;
@@ -976,7 +976,7 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
     const spin4d_adam_tensor& t = tensors[k];
     if (t.n < 0 || t.n > kMaxValues || !isfinite(t.lr) || !isfinite(t.weight_decay)) return SPIN4D_ERR_INVALID;
     if (!dtype_ok(t.grad_dtype)) return SPIN4D_ERR_INVALID;
-    if (t.params_work && ((t.work_dtype != SPIN4D_F16 && t.work_dtype != SPIN4D_BF16) || !array_ok(t.params_work, 1, 2)))
+    if (t.n && t.params_work && ((t.work_dtype != SPIN4D_F16 && t.work_dtype != SPIN4D_BF16) || !array_ok(t.params_work, 1, 2)))
       return SPIN4D_ERR_INVALID;
     if (!array_ok(t.params, t.n, 4) || !array_ok(t.m, t.n, 4) || !array_ok(t.v, t.n, 4) ||
         !array_ok(t.grad, t.n, dtype_bytes(t.grad_dtype)))

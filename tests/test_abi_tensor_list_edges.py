@@ -72,3 +72,14 @@ def test_adam_refuses_eps_outside_the_range_of_its_quotient(sp):
     assert statuses("spin4d_adam_step_tensors", [ADAM % x for x in taken]) == [sp.ERR_INJECTED] * len(taken)
     assert statuses("spin4d_adam_step_tensors", [ADAM % x for x in refused]) == [sp.ERR_INVALID] * len(refused)
     assert statuses("spin4d_adam_step_tensors", [ADAM % 1e-46]) == [sp.ERR_INJECTED]      # 0 in fp32
+
+
+def test_pointers_of_a_tensor_without_values_are_not_looked_at(sp):
+    """Odd and overlapping addresses of n = 0, with the types that go with them."""
+    odd = FAKE + 1
+    for w, wt in ((odd, 1), (FAKE, 0), (odd, 9)):
+        row = sp.AdamTensor(odd, w, odd, odd, odd, 0, 1e-3, 0.0, 0, wt)
+        assert sp.lib.spin4d_adam_step_tensors((sp.AdamTensor * 2)(row, row), 2, 1, 0.9, 0.99, 1e-8, 1, None, None,
+                                               None) == sp.OK
+    row = sp.GradTensor(odd, odd, 0, 0, 9)
+    assert sp.lib.spin4d_clip_grads((sp.GradTensor * 2)(row, row), 2, FAKE, None) == sp.OK
