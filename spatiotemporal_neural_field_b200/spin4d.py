@@ -603,7 +603,8 @@ def adam_step_tensors(tensors: AdamList, b1: float, b2: float, eps: float, step:
         _same_device(tensors, control)
         control_at = control.address
     if nonfinite_flag is not None:
-        if nonfinite_flag.get_device() != index or nonfinite_flag.dtype != torch.int32:
+        if (nonfinite_flag.get_device() != index or nonfinite_flag.dtype != torch.int32
+                or nonfinite_flag.numel() == 0):
             raise ValueError("the flag: an int32 value on the list's device")
         flag_at = nonfinite_flag.data_ptr()
     _list_call("spin4d_adam_step_tensors", index, stream,

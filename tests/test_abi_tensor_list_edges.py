@@ -8,6 +8,7 @@ import sys
 
 import numpy as np
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 1 << 20
@@ -83,3 +84,14 @@ def test_pointers_of_a_tensor_without_values_are_not_looked_at(sp):
                                                None) == sp.OK
     row = sp.GradTensor(odd, odd, 0, 0, 9)
     assert sp.lib.spin4d_clip_grads((sp.GradTensor * 2)(row, row), 2, FAKE, None) == sp.OK
+
+
+def test_adam_refuses_a_flag_without_a_value(sp, monkeypatch):
+    """An empty tensor's address is 0, which the library takes as no flag."""
+    lst = object.__new__(sp.AdamList)
+    lst.index, lst.count, lst.address = -1, 0, 0           # as CPU tensors number their device
+    monkeypatch.setattr(sp, "_list_call", lambda *args: None)
+    sp.adam_step_tensors(lst, 0.9, 0.99, 1e-8, step=1, nonfinite_flag=torch.zeros(1, dtype=torch.int32))
+    for flag in (torch.zeros(0, dtype=torch.int32), torch.zeros(1)):
+        with pytest.raises(ValueError):
+            sp.adam_step_tensors(lst, 0.9, 0.99, 1e-8, step=1, nonfinite_flag=flag)
