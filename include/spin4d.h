@@ -809,9 +809,11 @@ int spin4d_l2_window_clear(spin4d_stream_t stream);
 /*
  * 1 if this library was compiled with SPIN4D_CHECKED (libspin4d_checked.so),
  * else 0.  The checked build verifies on the device that every hash-table
- * index is below T and every HexPlane cell lies inside its plane; a failed
- * check is recorded and the access redirected to a valid address (nothing
- * traps), and spin4d_check_device_errors then returns SPIN4D_ERR_BOUNDS.
+ * index is below T, that every HexPlane cell lies inside its plane and, in the
+ * tensor-list calls, that a block's tiles belong to the tensor it takes them
+ * for, vectors lie inside it on their boundaries and partial sums in their
+ * workspace; a failed check is recorded and the access redirected to a valid
+ * address or left out (nothing traps), and spin4d_check_device_errors then returns SPIN4D_ERR_BOUNDS.
  */
 int spin4d_checked_build(void);
 

@@ -44,6 +44,16 @@ constexpr uint32_t kTensorTiles = 6;
 
 __host__ __device__ inline int dtype_bytes(int dt) { return dt == SPIN4D_F32 ? 4 : 2; }
 
+// What the checked build verifies on the device (a failure is recorded and the access left out or made value by value);
+// elsewhere it holds and costs nothing.
+__device__ __forceinline__ bool expect(bool ok) {
+#ifdef SPIN4D_CHECKED
+  return bounds_ok(ok);
+#else
+  return true;
+#endif
+}
+
 // ---------------------------------------------------------------------------
 // Lists as the kernels see them
 // ---------------------------------------------------------------------------
@@ -96,6 +106,11 @@ struct List {
 
   // The last tensor that begins at or before the tile: its owner (tensors without values own none).
   __device__ __forceinline__ int owner(uint32_t tile) const {
+    const int k = find(tile);
+    expect(tile >= tiles || (tile0[k] <= tile && tile < tile0[k + 1]));
+    return k;
+  }
+  __device__ __forceinline__ int find(uint32_t tile) const {
     if (CAP <= 16) {
       int k = 0;
       while (k + 1 < count && tile0[k + 1] <= tile) ++k;
@@ -202,6 +217,10 @@ struct Places {
       whole = first >= 0 && first + kVec <= n;
     }
   }
+  // whole places are one vector of an array that is aligned with them
+  __device__ __forceinline__ bool vector_in(const void* a, int bytes) const {
+    return ((uintptr_t)a + first * bytes) % (kVec * bytes) == 0;
+  }
   __device__ __forceinline__ int64_t place(int i) const { return first + (int64_t)i * stride; }
   __device__ __forceinline__ bool has(int i) const { return place(i) >= 0 && place(i) < n; }
 };
@@ -216,7 +235,7 @@ __device__ __forceinline__ void warm(const void* a, const Places& q, int bytes) 
 // bf16 gradients an odd value into their buffer: 79.8 us, aligned 77.9, every array a value at a time 90.7.)
 template <Hint H>
 __device__ __forceinline__ void fetch(const void* a, const Places& q, Raw<4>& r, bool loose = false) {
-  if (q.whole && !loose) {
+  if (q.whole && !loose && expect(q.vector_in(a, 4))) {
     load_raw<H>(static_cast<const float*>(a) + q.first, r);
   } else {
 #pragma unroll
@@ -225,7 +244,7 @@ __device__ __forceinline__ void fetch(const void* a, const Places& q, Raw<4>& r,
 }
 template <Hint H>
 __device__ __forceinline__ void fetch(const void* a, const Places& q, Raw<2>& r, bool loose = false) {
-  if (q.whole && !loose) {
+  if (q.whole && !loose && expect(q.vector_in(a, 2))) {
     load_raw<H>(static_cast<const uint16_t*>(a) + q.first, r);
   } else {
     uint32_t h[kVec];
@@ -236,7 +255,7 @@ __device__ __forceinline__ void fetch(const void* a, const Places& q, Raw<2>& r,
   }
 }
 __device__ __forceinline__ void put(void* a, const Places& q, const Raw<4>& r) {
-  if (q.whole) {
+  if (q.whole && expect(q.vector_in(a, 4))) {
     store_raw(static_cast<float*>(a) + q.first, r);
   } else {
 #pragma unroll
@@ -245,7 +264,7 @@ __device__ __forceinline__ void put(void* a, const Places& q, const Raw<4>& r) {
   }
 }
 __device__ __forceinline__ void put(void* a, const Places& q, const Raw<2>& r) {
-  if (q.whole) {
+  if (q.whole && expect(q.vector_in(a, 2))) {
     store_raw(static_cast<uint16_t*>(a) + q.first, r);
   } else {
 #pragma unroll
@@ -318,7 +337,14 @@ __device__ __forceinline__ double norm_of_tiles(const void* a, const Meta meta, 
   for (; t + kAhead <= whole; t += kAhead, at += kAhead * kTile * BYTES) {
     Raw<BYTES> r[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load_raw<kKeep>(at + u * kTile * BYTES, r[u]);
+    for (int u = 0; u < kAhead; ++u) {
+      const char* const from = at + u * kTile * BYTES;
+      const Places q(t + u, shift, n);
+      if (expect(q.whole && from == static_cast<const char*>(a) + q.first * BYTES && q.vector_in(a, BYTES)))
+        load_raw<kKeep>(from, r[u]);
+      else
+        fetch<kKeep>(a, q, r[u], true);
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       float x[kVec];
@@ -386,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, kNormBlocks) norm_kernel(const __gri
   }
   pdl_wait();
   pdl_release();
+  const int slots = list.tiles == 0 ? 0 : gridDim.x + (f.norms ? list.count - 1 : 0);
   double acc = 0.0;
   int parts = 0;
   // the warps walk through the block's tensors on their own; they meet when the parts are written out
@@ -395,12 +422,13 @@ __global__ void __launch_bounds__(kThreads, kNormBlocks) norm_kernel(const __gri
       double s = part[threadIdx.x][0];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) s = join<NORM>(s, part[threadIdx.x][w]);
-      f.slots[part_slot[threadIdx.x]] = s;
+      // (a list without values has one block, whose slot nobody reads)
+      if (expect(part_slot[threadIdx.x] >= 0 && part_slot[threadIdx.x] < max(slots, 1))) f.slots[part_slot[threadIdx.x]] = s;
     }
     __syncthreads();
     parts = 0;
   };
-  for (int k = owner; t < end; ++k) {
+  for (int k = owner; t < end && expect(k < list.count); ++k) {
     const uint32_t base = list.tile0[k], stop = min(end, list.tile0[k + 1]);
     if (t >= stop) continue;                  // a tensor without values
     const void* a = list.at[k].a;
@@ -443,7 +471,6 @@ __global__ void __launch_bounds__(kThreads, kNormBlocks) norm_kernel(const __gri
   // All slots at once into shared memory: what follows is sums of few terms in a fixed order.
   constexpr int kSlotLoads = (kMaxNormBlocks + CAP + kThreads - 1) / kThreads;
   constexpr int kTileLoads = CAP > 16 ? CAP / kThreads + 1 : 0;
-  const int slots = list.tiles == 0 ? 0 : gridDim.x + (f.norms ? list.count - 1 : 0);
   const int starts = f.norms ? list.count + 1 : 0;
   double slot[kSlotLoads];
   uint32_t start[kTileLoads + 1];
@@ -479,11 +506,12 @@ __global__ void __launch_bounds__(kThreads, kNormBlocks) norm_kernel(const __gri
     f.norms[k] = (float)(f.grad_scale * (NORM == kL2 ? sqrt(s) : s));
     mine = join<NORM>(mine, s);
   };
+  auto slot_sum = [&](int i) { return expect(i >= 0 && i < slots) ? sums[i] : 0.0; };
   auto by_warp = [&](int k, uint32_t a, uint32_t e) {
     double s = 0.0;
     if (e > a) {
       const int b1 = (e - 1) / per;
-      for (int b = a / per + lane; b <= b1; b += 32) s = join<NORM>(s, sums[b + k]);
+      for (int b = a / per + lane; b <= b1; b += 32) s = join<NORM>(s, slot_sum(b + k));
     }
     s = lanes_join<NORM, 32>(s);
     if (lane == 0) finish_tensor(k, s);
@@ -500,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, kNormBlocks) norm_kernel(const __gri
       double s = 0.0;
       if (e > a) {
         const int b1 = (e - 1) / per;
-        for (int b = a / per; b <= b1; ++b) s = join<NORM>(s, sums[b + k]);
+        for (int b = a / per; b <= b1; ++b) s = join<NORM>(s, slot_sum(b + k));
       }
       finish_tensor(k, s);
     }
@@ -570,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
   const uint32_t begin = (gridDim.x - 1 - blockIdx.x) * list.per;
   uint32_t end = min(list.tiles, begin + list.per);
   const float coef = control->coef;
-  for (int k = list.owner(end - 1); end > begin; --k) {
+  for (int k = list.owner(end - 1); end > begin && expect(k >= 0); --k) {
     const uint32_t base = list.tile0[k], t = max(begin, base);
     if (t >= end) continue;                   // a tensor without values
     const ClipEntry& e = list.at[k];
@@ -627,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 3) adam_list_kernel(const __grid_con
   pdl_release();
   float coef = 1.0f, inv_bc1 = 0.0f, inv_bc2 = 0.0f;
   bool ready = false, skip = false, bad = false;
-  for (int k = last; end > begin; --k) {
+  for (int k = last; end > begin && expect(k >= 0); --k) {
     const uint32_t base = list.tile0[k], stop = max(begin, base);
     if (stop >= end) continue;                // a tensor without values
     const AdamEntry& e = list.at[k];
@@ -976,7 +1004,8 @@ extern "C" int spin4d_adam_step_tensors(const spin4d_adam_tensor* tensors, int c
     const spin4d_adam_tensor& t = tensors[k];
     if (t.n < 0 || t.n > kMaxValues || !isfinite(t.lr) || !isfinite(t.weight_decay)) return SPIN4D_ERR_INVALID;
     if (!dtype_ok(t.grad_dtype)) return SPIN4D_ERR_INVALID;
-    if (t.n && t.params_work && ((t.work_dtype != SPIN4D_F16 && t.work_dtype != SPIN4D_BF16) || !array_ok(t.params_work, 1, 2)))
+    if (t.n && t.params_work &&
+        ((t.work_dtype != SPIN4D_F16 && t.work_dtype != SPIN4D_BF16) || !array_ok(t.params_work, t.n, 2)))
       return SPIN4D_ERR_INVALID;
     if (!array_ok(t.params, t.n, 4) || !array_ok(t.m, t.n, 4) || !array_ok(t.v, t.n, 4) ||
         !array_ok(t.grad, t.n, dtype_bytes(t.grad_dtype)))
