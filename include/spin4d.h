@@ -328,18 +328,20 @@ size_t spin4d_grad_norm_workspace(int count);
 /*
  * norm = the norm of grad_scale * g over all tensors of the list, and
  *   coef = grad_scale * min(1, max_norm / (norm + 1e-6)).
- * grad_scale (in fp32 > 0 and finite) undoes a loss scale or averages a sum over ranks;
- * max_norm >= 0, INFINITY to measure only.  Where the norm is not a finite
- * fp32 number (a NaN or infinity in any gradient), coef is 0, `step` stays and
- * `skipped` counts it.  norms (optional, `count` fp32 values): each tensor's
- * own norm, likewise scaled.  Squares and sums are 64-bit and are added in an
- * order that the lengths, types and alignments of the list and the device
- * alone determine: the same gradients give the same bits.  A tensor listed
- * twice counts twice.
+ * grad_scale (in fp32 > 0 and finite) undoes a loss scale or averages a sum
+ * over ranks; max_norm >= 0, INFINITY to measure only.  Where the norm is not a
+ * finite fp32 number (a NaN or infinity in any gradient), coef is 0, `step`
+ * stays and `skipped` counts it.  coef is rounded to fp32: below 2^-126 it has
+ * fewer bits, and below 2^-150 it is 0, which clips a finite gradient to zeros
+ * and still counts as a step.  norms (optional, `count` fp32 values): each
+ * tensor's own norm, likewise scaled.  Squares and sums are 64-bit and are
+ * added in an order that the lengths, types and alignments of the list, the
+ * device and whether `norms` is given determine: the same call on the same
+ * gradients gives the same bits.  A tensor listed twice counts twice.
  *   workspace  device, spin4d_grad_norm_workspace(count) bytes, 256-byte
  *              aligned, contents ignored on entry; calls that can overlap on
  *              the GPU (other streams, captured graphs) need one each
- * count == 0 measures nothing: norm 0, coef grad_scale (0 for max_norm == 0).
+ * count == 0 measures nothing: norm 0 and the coef that goes with it.
  */
 int spin4d_grad_norm(const spin4d_grad_tensor* tensors, int count, int norm_type, double grad_scale,
                      double max_norm, spin4d_grad_control* control, float* norms,
@@ -349,6 +351,8 @@ int spin4d_grad_norm(const spin4d_grad_tensor* tensors, int count, int norm_type
  * out = control->coef * grad for every tensor, in fp32 and rounded to the
  * output's type; coef == 0 writes zeros whatever the gradient holds, so that a
  * gradient with a NaN is dropped whole.  In place, coef == 1 writes nothing.
+ * What it has written is not for spin4d_adam_step_tensors with the same
+ * control, which would apply coef again.
  * SPIN4D_ERR_INVALID when an output overlaps another array of the list (its
  * own gradient in the same type, that is in place, excepted).
  */
@@ -377,8 +381,13 @@ typedef struct spin4d_adam_tensor {
  *   m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2;
  *   p -= lr * (m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps) + lr * weight_decay * p
  * t = step when step > 0, else control->step (which spin4d_grad_norm has
- * advanced).  The square root is within 2^-23 of itself and the quotient within
- * 2 ulp; for that eps is 0 or, in fp32, from 2^-126 to 2^125.  Where control->norm is not finite (or t < 1) params, params_work, m
+ * advanced).  The rates are read during the call like the rest of the list: a
+ * captured call keeps them, and one under a schedule takes a list with the new
+ * ones.  The square root is within 2^-23 of itself, 1 - b^t within 2^-22 and the
+ * quotient within 2 ulp; for that eps is 0 or, in fp32, from 2^-126 to 2^125.
+ * (spin4d_adam_step, for one fp32 gradient, rounds root and quotient correctly
+ * and has 1 - b^t in 64 bits; it is the one to use where that last bit of the
+ * step counts.)  Where control->norm is not finite (or t < 1) params, params_work, m
  * and v stay as they are.  zero_grad != 0 clears the gradients in either
  * case.  nonfinite_flag as in spin4d_adam_step.  SPIN4D_ERR_INVALID when an
  * array that is written overlaps another one of the list; gradients that are

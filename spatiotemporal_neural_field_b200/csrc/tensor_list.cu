@@ -286,8 +286,9 @@ __device__ __forceinline__ void put(void* a, int dt, const Places& q, const floa
 
 // ---------------------------------------------------------------------------
 // Norm.  Squares and sums are 64-bit: a square of any fp32 value and the sum
-// of 2^40 of them neither overflow nor vanish, and the sum's order does not
-// show in the 32-bit result.  No atomics on sums: block b's part of tensor k
+// of 2^40 of them neither overflow nor vanish.  The sum's order (another one
+// where `norms` is given) shows in the 32-bit result only where that lies a
+// 64-bit rounding from the middle between two numbers.  No atomics on sums: block b's part of tensor k
 // goes to slot b + k (along the walk over (b, k) one of the two grows at each
 // part, so no two parts share a slot), and the block that finishes last adds
 // the slots in a fixed order, whichever block that is.
@@ -602,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
     const uint32_t base = list.tile0[k], t = max(begin, base);
     if (t >= end) continue;                   // a tensor without values
     const ClipEntry& e = list.at[k];
-    // in place and within bounds, as in most steps: every value would be written back as it is (16.8M fp32 with
-    // the norm 18.8 us)
+    // in place and within bounds, as in most steps: every value would be written back as it is (norm and clip of 16.8M
+    // fp32 values 19.3 us, with a coefficient below 1 31.4)
     if (coef != 1.0f || e.out != e.a) {
       if (e.meta.dtype() == SPIN4D_F32) clip_tiles<4>(e.a, e.out, e.meta, t - base, end - base, coef);
       else clip_tiles<2>(e.a, e.out, e.meta, t - base, end - base, coef);
@@ -615,14 +616,15 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Adam with decoupled weight decay, formula in the header.  Four streams in,
 // three and the working copy out: bound by HBM, 134M parameters with fp16
-// copies (30 bytes each) in 595 us, 6.8 TB/s; 16.8M in 74.  72 registers for 128
+// copies (30 bytes each) in 595 us, 6.8 TB/s; 16.8M in 74.  72 to 74 registers for 128
 // bytes of loads a thread, three blocks a SM; the first loads are on their way
 // before the control block is read, and in L2 before the norm has ended.
 // ---------------------------------------------------------------------------
 // The square root within 2^-23 of itself (subnormal arguments too).  With it and a quotient within 2 ulp a step
 // is off by at most 2^-22 of what it moves a parameter more than with the correctly rounded ones, of which the
-// parameter's own rounding usually leaves nothing.  Those took most of the kernel's instructions: norm and update
-// of 16.8M parameters 101.4 us, of the smallest decoder 8.0; so 89.6 and 6.4.
+// parameter's own rounding usually leaves nothing.  Those took most of the kernel's instructions, and more where
+// the state of untouched entries has decayed below 2^-126.  Norm and update with them of the smallest decoder 7.8 us, of
+// 200 tensors 15.8, of 16.8M parameters 89 to 105, of 134M 693 to 746; so 6.0, 13.2, 87 and 687 (from graphs).
 __device__ __forceinline__ float root(float x) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -864,6 +866,11 @@ int norm_launches(const spin4d_grad_tensor* ts, int count, NormArgs f, cudaStrea
   return SPIN4D_OK;
 }
 
+// A launch costs the host by the size of its parameters, and the norm's finish by the capacity: lists have the smallest
+// capacity that holds them.  The largest fill what a launch can carry (32 KB).  The steps below them, us a call through
+// the binding (the next larger capacity in brackets): norm of 16 tensors 4.9, of 40 5.2 (5.2), of 65 5.4 (5.8), of 300
+// 7.1 (7.65); clip of 2 3.1 (with the largest 4.3), of 40 3.7 (3.9), of 65 4.0 (4.7), of 300 5.4 (6.1); Adam of 40 5.4
+// (5.6), of 65 5.9 (6.4), of 200 7.5 (7.8).  320 keeps clip's parameters below 10 KB, 224 is half of Adam's largest.
 template <int NORM>
 int norm_list(const spin4d_grad_tensor* ts, int count, const NormArgs& f, cudaStream_t s) {
   if (count <= 16) return norm_launches<16, NORM>(ts, count, f, s);

@@ -445,7 +445,8 @@ def _same_lengths(lengths, others, what: str) -> None:
 
 class GradList(_TensorList):
     """Gradients (float32, float16 or bfloat16) for grad_norm and clip_grads,
-    with the outputs that clip_grads writes (None: in place)."""
+    with the outputs that clip_grads writes (None: in place).  A parameter
+    without a gradient is left out: None is not a gradient."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[Optional[torch.Tensor]]] = None):
         grads = list(grads)
@@ -491,7 +492,8 @@ def grad_list(grads, outs=None) -> GradList:
 def adam_list(params, grads, m, v, lr, weight_decay=0.0, params_work=None) -> AdamList:
     """Parameters (float32), gradients (float32, float16, bfloat16), Adam's m
     and v (float32) and the optional float16 or bfloat16 working copies.  lr
-    and weight_decay: one number, or one for each tensor."""
+    and weight_decay: one number, or one for each tensor.  They belong to the
+    list: another rate takes another list, and a captured step keeps its own."""
     return AdamList(params, grads, m, v, lr, weight_decay, params_work)
 
 
@@ -581,7 +583,8 @@ def grad_norm(grads, control: GradControl, max_norm: float = float("inf"), norm_
 
 def clip_grads(grads, control: GradControl, stream=None) -> None:
     """Multiplies every gradient by ``control.coef``, in place or into the
-    list's outputs; a coefficient of 0 writes zeros."""
+    list's outputs; a coefficient of 0 writes zeros.  (adam_step_tensors with
+    ``control`` applies the coefficient by itself, to gradients not yet clipped.)"""
     if type(grads) is not GradList:
         grads = GradList(grads)
     _same_device(grads, control)
