@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from .spin4d import Spin4dError, _check, _ptr, _stream, c_i32, c_i64, c_u32, c_vp
+from .spin4d import Spin4dError, _check, _on, _ptr, _stream, c_i32, c_i64, c_u32, c_vp
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspin4d_probe.so")
 if not os.path.exists(_LIB_PATH):
@@ -43,7 +43,8 @@ def probe_gather(buf: torch.Tensor, width: int, loads_per_thread: int, blocks: i
     """Launches the random-gather probe; returns the number of `width`-byte
     units read (sectors for width 4/16, 128-byte lines for width 128)."""
     if sink is None:
-        sink = torch.zeros(1, dtype=torch.int32, device=buf.device)
+        with _on(stream, buf.device):
+            sink = torch.zeros(1, dtype=torch.int32, device=buf.device)
     _check("spin4d_probe_gather", lib.spin4d_probe_gather(_ptr(buf), buf.numel() * buf.element_size(), width,
                                                           loads_per_thread, blocks, seed, _ptr(sink),
                                                           _stream(stream)))
@@ -70,7 +71,8 @@ def probe_stream(buf: torch.Tensor, passes: int, blocks: int, sink: Optional[tor
                  stream=None) -> int:
     """Sequential-read probe; returns the bytes read."""
     if sink is None:
-        sink = torch.zeros(1, dtype=torch.int32, device=buf.device)
+        with _on(stream, buf.device):
+            sink = torch.zeros(1, dtype=torch.int32, device=buf.device)
     nbytes = buf.numel() * buf.element_size()
     _check("spin4d_probe_stream", lib.spin4d_probe_stream(_ptr(buf), nbytes, passes, blocks, _ptr(sink),
                                                           _stream(stream)))
@@ -80,7 +82,8 @@ def probe_stream(buf: torch.Tensor, passes: int, blocks: int, sink: Optional[tor
 def probe_fma(iters: int, blocks: int, device, sink: Optional[torch.Tensor] = None, stream=None) -> int:
     """fp32 FMA-chain probe; returns the FLOPs executed."""
     if sink is None:
-        sink = torch.zeros(1, dtype=torch.int32, device=device)
+        with _on(stream, device):
+            sink = torch.zeros(1, dtype=torch.int32, device=device)
     _check("spin4d_probe_fma", lib.spin4d_probe_fma(iters, blocks, _ptr(sink), _stream(stream)))
     return 16 * iters * blocks * 256
 

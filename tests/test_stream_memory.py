@@ -197,3 +197,16 @@ def test_render_on_a_stream_grows_its_state_and_gives_the_image(sp):
     torch.cuda.synchronize()
     assert grown is not state and grown.max_pairs == full.pairs_needed()
     assert torch.equal(got, want)
+
+
+def test_probes_allocate_their_sinks_on_the_stream_they_run_on(sp, seen, monkeypatch):
+    from spatiotemporal_neural_field_b200 import probe
+    monkeypatch.setattr(probe, "lib", FakeLib())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: Side())
+    buf, side = torch.Tensor(64), Side()
+    for stream, want in ((None, None), (side, side)):
+        del seen[:]
+        probe.probe_gather(buf, 4, 8, 1, stream=stream)
+        probe.probe_stream(buf, 1, 1, stream=stream)
+        probe.probe_fma(1, 1, "cpu", stream=stream)
+        assert seen == [("zeros", want)] * 3
