@@ -221,8 +221,8 @@ def _on(stream, device):
     ordered along the stream it was taken on; of the current stream's, work that is pending there may still be using it."""
     if stream is None:
         return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        handle = int(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
         # 0 and 1: the handles of the legacy default stream
         stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
     return torch.cuda.stream(stream)

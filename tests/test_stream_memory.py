@@ -12,8 +12,11 @@ from tests import tol
 
 
 class Side:
-    """A stream by its handle, as torch.cuda.Stream has it."""
+    """Another library's stream object, known by its handle."""
     cuda_stream = 0x5000
+
+
+SIDE = ("external", 0x5000)
 
 
 @pytest.fixture(scope="module")
@@ -51,6 +54,8 @@ def seen(sp, monkeypatch):
         monkeypatch.setattr(owner, name, noted)
 
     monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
     monkeypatch.setattr(torch.cuda, "device", lambda index: contextlib.nullcontext())
     monkeypatch.setattr(sp, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(sp, "_current_device", lambda: -1)
@@ -70,9 +75,7 @@ def control(sp):
 def test_grad_norm_allocates_its_workspace_on_the_stream_of_the_call(sp, seen, monkeypatch):
     grads, ctl, side = sp.grad_list([]), control(sp), Side()
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
-    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
-    for stream, want in ((None, None), (side, side), (0x7000, ("external", 0x7000)), (0, "default"), (1, "default")):
+    for stream, want in ((None, None), (side, SIDE), (0x7000, ("external", 0x7000)), (0, "default"), (1, "default")):
         del seen[:]
         sp.grad_norm(grads, ctl, stream=stream)
         assert seen == [("empty", want)]
@@ -136,7 +139,7 @@ def test_calls_allocate_on_the_stream_they_run_on(sp, seen, monkeypatch, name):
     call, count = calls(sp)[name]
     side = Side()
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: Side())
-    for stream, want in ((None, None), (side, side)):
+    for stream, want in ((None, None), (side, SIDE)):
         del seen[:]
         call(stream)
         assert [w for _, w in seen] == [want] * count
@@ -167,7 +170,7 @@ def test_render_reads_the_pair_count_on_the_stream_of_the_call(sp, seen, monkeyp
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: Side())
     cam, desc = sp.camera([[1, 0, 0, 0], [0, 1, 0, 0], [0, 0, 1, 0]], 1, 1, 0, 0, 32, 16), sp.render_desc()
     t, side = torch.Tensor, Side()
-    for stream, want in ((None, None), (side, side)):
+    for stream, want in ((None, None), (side, SIDE)):
         state = object.__new__(sp.RenderState)
         state.buf, state.max_pairs = torch.zeros(64, dtype=torch.uint8), 1 << 20
         del seen[:]
@@ -204,9 +207,23 @@ def test_probes_allocate_their_sinks_on_the_stream_they_run_on(sp, seen, monkeyp
     monkeypatch.setattr(probe, "lib", FakeLib())
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: Side())
     buf, side = torch.Tensor(64), Side()
-    for stream, want in ((None, None), (side, side)):
+    for stream, want in ((None, None), (side, SIDE)):
         del seen[:]
         probe.probe_gather(buf, 4, 8, 1, stream=stream)
         probe.probe_stream(buf, 1, 1, stream=stream)
         probe.probe_fma(1, 1, "cpu", stream=stream)
         assert seen == [("zeros", want)] * 3
+
+
+@pytest.mark.gpu
+def test_streams_by_object_and_by_handle(sp):
+    """A torch stream, another library's object with its handle, the handle itself, and the default stream's handles."""
+    g = torch.full((5000,), 0.5, device="cuda")
+    grads, ctl, side = sp.grad_list([g]), sp.grad_control(), torch.cuda.Stream()
+    other = Side()
+    other.cuda_stream = side.cuda_stream
+    torch.cuda.synchronize()
+    for i, stream in enumerate((side, other, side.cuda_stream, 0, 1)):
+        sp.grad_norm(grads, ctl, max_norm=1.0, stream=stream)
+        torch.cuda.synchronize()
+        assert int(ctl.step) == 1 + i and abs(float(ctl.norm) - 1250 ** 0.5) <= 2.0 ** -24 * 64
